@@ -1,6 +1,8 @@
 // C entry points of libress.so: argument validation on the host, then kernel launches on
 // the caller's stream.  Validation happens before any CUDA call, so a bad argument is
 // reported without touching the device.
+#include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -43,6 +45,55 @@ ress_status check_shape(const ress_shape *s, Dims *d, bool *empty) {
 bool ptr_ok(const void *p) { return p != nullptr && aligned16(p); }
 
 ress_status from_cuda(cudaError_t e) { return e == cudaSuccess ? RESS_OK : RESS_ERR_CUDA; }
+
+bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+// ------------------------------------------------------------ checks of the token operators
+size_t dtype_bytes(int32_t dtype) {
+  return dtype == RESS_BF16 || dtype == RESS_FP16 ? 2 : (dtype == RESS_FP32 ? 4 : 0);
+}
+
+bool plan_ok(const ress_rope_plan *r) {
+  if (r == nullptr || r->head_dim < 2 || r->head_dim > RESS_MAX_TOKEN_DIM) return false;
+  if (r->axes < 1 || r->axes > 3 || r->rot_dim < 2 || r->rot_dim > r->head_dim) return false;
+  if (r->rot_dim % (2 * r->axes) != 0) return false;
+  if (r->layout != RESS_ROPE_HALF && r->layout != RESS_ROPE_INTERLEAVED) return false;
+  return r->amplitude > 0.f && !std::isinf(r->amplitude);
+}
+
+bool positions_ok(const ress_rope_plan *r, const int32_t *positions, int64_t stride_b) {
+  if (positions == nullptr) return r->axes == 1;
+  return aligned_to(positions, 4) && stride_b >= 0;
+}
+
+bool rows_ok(const ress_rows *r, size_t size) {
+  return r != nullptr && r->ptr != nullptr && aligned_to(r->ptr, size) && r->stride_b >= 0 &&
+         r->stride_h >= 0 && r->stride_t >= 0;
+}
+
+// An output view: its rows of `dim` elements must not overlap.  Taken from the smallest
+// stride up, each stride has to reach past everything that the smaller ones span.
+bool out_rows_ok(const ress_rows *r, size_t size, int64_t batch, int64_t heads, int64_t tokens,
+                 int64_t dim) {
+  if (!rows_ok(r, size)) return false;
+  struct Axis {
+    int64_t stride, count;
+  } ax[3] = {{r->stride_b, batch}, {r->stride_h, heads}, {r->stride_t, tokens}};
+  std::sort(ax, ax + 3, [](const Axis &x, const Axis &y) { return x.stride < y.stride; });
+  int64_t span = dim;
+  for (const Axis &x : ax) {
+    if (x.count == 1) continue;
+    if (x.stride < span || x.stride > ((int64_t)1 << 60) / x.count) return false;
+    span += x.stride * (x.count - 1);
+  }
+  return true;
+}
+
+// Two views of one pointer that name the same rows (strides of single entries do not count).
+bool same_rows(const ress_rows *x, const ress_rows *y, int64_t batch, int64_t heads, int64_t tokens) {
+  return (batch == 1 || x->stride_b == y->stride_b) && (heads == 1 || x->stride_h == y->stride_h) &&
+         (tokens == 1 || x->stride_t == y->stride_t);
+}
 
 }  // namespace
 
@@ -384,6 +435,135 @@ ress_status ress_debug_attn_forced_timeout(const ress_shape *shape, const void *
   cudaError_t e = ress::launch_attn(d, a, (cudaStream_t)stream);
   if (e == cudaErrorNotSupported) return RESS_ERR_CUDA;
   return from_cuda(e);
+}
+
+// ------------------------------------------------------------------- token operators
+ress_status ress_rope_init(ress_rope_plan *plan, int32_t head_dim, int32_t rot_dim, int32_t axes,
+                           int32_t layout, double theta, int32_t scaling, double factor,
+                           int32_t original_len, double beta_fast, double beta_slow) {
+  if (plan == nullptr || !(theta > 1.0 && theta <= 1e12)) return RESS_ERR_INVALID_ARG;
+  if (scaling < RESS_ROPE_PLAIN || scaling > RESS_ROPE_YARN) return RESS_ERR_INVALID_ARG;
+  if (scaling != RESS_ROPE_PLAIN && !(factor >= 1.0 && factor <= 1e6)) return RESS_ERR_INVALID_ARG;
+  if (scaling == RESS_ROPE_YARN &&
+      (original_len < 1 || !(beta_slow > 0.0) || !(beta_slow < beta_fast) || std::isinf(beta_fast)))
+    return RESS_ERR_INVALID_ARG;
+  ress_rope_plan r = {};
+  r.head_dim = head_dim;
+  r.rot_dim = rot_dim;
+  r.axes = axes;
+  r.layout = layout;
+  r.amplitude = scaling == RESS_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+  if (!plan_ok(&r)) return RESS_ERR_INVALID_ARG;
+  const int d = rot_dim / axes;
+  if (scaling == RESS_ROPE_NTK && d <= 2) return RESS_ERR_INVALID_ARG;
+  const long double pi2 = 6.28318530717958647692528676655900577L;
+  long double base = theta;
+  if (scaling == RESS_ROPE_NTK) base *= powl((long double)factor, (long double)d / (d - 2));
+  // YaRN: pair index at which a pair turns `turns` times within the trained length
+  auto pair_of = [&](double turns) {
+    return d * std::log(original_len / (turns * (double)pi2)) / (2.0 * std::log(theta));
+  };
+  double low = 0.0, high = 0.0;
+  if (scaling == RESS_ROPE_YARN) {
+    low = std::max(std::floor(pair_of(beta_fast)), 0.0);
+    high = std::min(std::ceil(pair_of(beta_slow)), d - 1.0);
+  }
+  for (int i = 0; i < d / 2; ++i) {
+    long double f = powl(base, -2.0L * i / d);
+    if (scaling == RESS_ROPE_LINEAR) f /= factor;
+    if (scaling == RESS_ROPE_YARN) {
+      const double ramp = std::min(std::max((i - low) / std::max(high - low, 0.001), 0.0), 1.0);
+      f = f / factor * ramp + f * (1.0 - ramp);
+    }
+    // f <= 1 radian per position: a fraction of a turn below 0.16
+    r.phase[i] = (uint64_t)roundl(f / pi2 * 18446744073709551616.0L);
+  }
+  *plan = r;
+  return RESS_OK;
+}
+
+ress_status ress_rope(const ress_rope_plan *plan, int32_t batch, int32_t heads, int32_t tokens,
+                      int32_t dtype, const ress_rows *x, const int32_t *positions,
+                      int64_t pos_stride_b, int32_t inverse, const ress_rows *out,
+                      ress_stream_t stream) {
+  if (!plan_ok(plan) || batch < 0 || heads < 0 || tokens < 0) return RESS_ERR_INVALID_ARG;
+  if (inverse != 0 && inverse != 1) return RESS_ERR_INVALID_ARG;
+  const size_t size = dtype_bytes(dtype);
+  if (size == 0 || !positions_ok(plan, positions, pos_stride_b)) return RESS_ERR_INVALID_ARG;
+  if (batch == 0 || heads == 0 || tokens == 0) return RESS_OK;
+  if (!rows_ok(x, size) || !out_rows_ok(out, size, batch, heads, tokens, plan->head_dim))
+    return RESS_ERR_INVALID_ARG;
+  if (x->ptr == out->ptr && !same_rows(x, out, batch, heads, tokens)) return RESS_ERR_INVALID_ARG;
+  ress::TokensLaunch a = {};
+  a.parts = 1;
+  a.batch = batch;
+  a.tokens = tokens;
+  a.head_dim = plan->head_dim;
+  a.dtype = dtype;
+  a.norm = RESS_NORM_NONE;
+  a.rope = plan;
+  a.inverse = inverse != 0;
+  a.positions = positions;
+  a.pos_stride_b = pos_stride_b;
+  a.views = 1;
+  a.part[0] = {x, out, heads, true, nullptr, nullptr};
+  return from_cuda(ress::launch_tokens(a, (cudaStream_t)stream));
+}
+
+ress_status ress_qk_norm_rope(const ress_qk_params *params, const ress_rows *q,
+                              const ress_rows *k, const ress_rows *v, const ress_rows *q_out,
+                              const ress_rows *k_out, const ress_rows *v_out,
+                              ress_stream_t stream) {
+  if (params == nullptr) return RESS_ERR_INVALID_ARG;
+  const ress_qk_params &p = *params;
+  if (p.batch < 0 || p.tokens < 0 || p.q_heads < 1 || p.kv_heads < 1) return RESS_ERR_INVALID_ARG;
+  if (p.head_dim < 2 || p.head_dim > RESS_MAX_TOKEN_DIM) return RESS_ERR_INVALID_ARG;
+  const size_t size = dtype_bytes(p.dtype);
+  if (size == 0) return RESS_ERR_INVALID_ARG;
+  if (p.norm < RESS_NORM_NONE || p.norm > RESS_NORM_LAYER) return RESS_ERR_INVALID_ARG;
+  if (!(p.eps >= 0.f) || std::isinf(p.eps)) return RESS_ERR_INVALID_ARG;
+  for (const float *w : {p.q_weight, p.q_bias, p.k_weight, p.k_bias})
+    if (!aligned_to(w, 4)) return RESS_ERR_INVALID_ARG;
+  if (p.rope != nullptr) {
+    if (!plan_ok(p.rope) || p.rope->head_dim != p.head_dim) return RESS_ERR_INVALID_ARG;
+    if (!positions_ok(p.rope, p.positions, p.pos_stride_b)) return RESS_ERR_INVALID_ARG;
+  }
+  if (p.views < 1 || p.specials < 0 || p.tokens % p.views != 0 || p.specials > p.tokens / p.views)
+    return RESS_ERR_INVALID_ARG;
+  if ((v == nullptr) != (v_out == nullptr)) return RESS_ERR_INVALID_ARG;
+  if (p.batch == 0 || p.tokens == 0) return RESS_OK;
+  const bool moves = p.specials > 0 && p.specials < p.tokens / p.views;  // some token's place changes
+  const ress_rows *in[3] = {q, k, v}, *out[3] = {q_out, k_out, v_out};
+  const int heads[3] = {p.q_heads, p.kv_heads, p.kv_heads};
+  const int parts = v != nullptr ? 3 : 2;
+  for (int i = 0; i < parts; ++i) {
+    if (!rows_ok(in[i], size) || !out_rows_ok(out[i], size, p.batch, heads[i], p.tokens, p.head_dim))
+      return RESS_ERR_INVALID_ARG;
+    for (int j = 0; j < parts; ++j) {
+      if (in[j] == nullptr || in[j]->ptr != out[i]->ptr) continue;
+      if (i != j || moves || !same_rows(in[i], out[i], p.batch, heads[i], p.tokens))
+        return RESS_ERR_INVALID_ARG;
+    }
+    for (int j = 0; j < i; ++j)
+      if (out[i]->ptr == out[j]->ptr) return RESS_ERR_INVALID_ARG;
+  }
+  ress::TokensLaunch a = {};
+  a.parts = parts;
+  a.batch = p.batch;
+  a.tokens = p.tokens;
+  a.head_dim = p.head_dim;
+  a.dtype = p.dtype;
+  a.norm = p.norm;
+  a.eps = p.eps;
+  a.rope = p.rope;
+  a.positions = p.positions;
+  a.pos_stride_b = p.pos_stride_b;
+  a.views = p.views;
+  a.specials = p.specials;
+  a.part[0] = {q, q_out, heads[0], true, p.q_weight, p.q_bias};
+  a.part[1] = {k, k_out, heads[1], true, p.k_weight, p.k_bias};
+  a.part[2] = {v, v_out, heads[2], false, nullptr, nullptr};
+  return from_cuda(ress::launch_tokens(a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -91,4 +91,23 @@ struct AttnLaunch {
 // Returns cudaErrorNotSupported if the driver cannot encode tensor maps.
 cudaError_t launch_attn(const Dims &d, const AttnLaunch &a, cudaStream_t st);
 
+// Per-head norm, rotation and move of up to three tensors (q, k, v), token by token.
+struct TokensPart {
+  const ress_rows *in, *out;
+  int heads;
+  bool work;  // norm and rotate; false: move only
+  const float *weight, *bias;
+};
+struct TokensLaunch {
+  int parts, batch, tokens, head_dim, dtype, norm;
+  float eps;
+  const ress_rope_plan *rope;  // or null
+  bool inverse;
+  const int32_t *positions;
+  long long pos_stride_b;
+  int views, specials;  // token order of the outputs
+  TokensPart part[3];
+};
+cudaError_t launch_tokens(const TokensLaunch &a, cudaStream_t st);
+
 }  // namespace ress

@@ -55,6 +55,25 @@ class SparseGlobalAttention:
         """M_h = W_O^h^T W_O^h for every head (ReSS Eq. 8), computed once per layer."""
         R.ress_head_gram(self.shape, w_o.contiguous().float(), self.gram, stream)
 
+    def prepare(self, packed, plan=None, positions=None, norm: int = R.NORM_NONE, eps: float = 1e-6,
+                q_weight=None, q_bias=None, k_weight=None, k_bias=None, views: int = 1,
+                specials: int = 0, stream=None):
+        """q, k, v [B,H,N,64] of the path from the layer's packed projection [B,N,3,H,64]: the
+        per-head norm and the rotary positions of q and k, and the move of every view's
+        special tokens to the tail, in one pass.  The three tensors belong to the layer and
+        are overwritten by the next call."""
+        if getattr(self, "_qkv", None) is None:
+            self._qkv = [torch.empty(self.B, self.H, self.N, 64, device=self.device,
+                                     dtype=torch.bfloat16) for _ in range(3)]
+        if packed.shape != (self.B, self.N, 3, self.H, 64):
+            raise ValueError(f"expected a packed projection [B,N,3,H,64], got {tuple(packed.shape)}")
+        q, k, v = (packed[:, :, i].transpose(1, 2) for i in range(3))
+        q_out, k_out, v_out = self._qkv
+        R.ress_qk_norm_rope(q, k, q_out, k_out, v, v_out, norm=norm, eps=eps, q_weight=q_weight,
+                            q_bias=q_bias, k_weight=k_weight, k_bias=k_bias, plan=plan,
+                            positions=positions, views=views, specials=specials, stream=stream)
+        return q_out, k_out, v_out
+
     # ------------------------------------------------------------------ the path
     def pool(self, q, k, v, stream=None):
         R.ress_pool_blocks(self.shape, q, k, v, self.q_pool, self.k_pool, self.v_pool, stream)

@@ -23,6 +23,11 @@ STATUS_NAMES = {0: "RESS_OK", 1: "RESS_ERR_INVALID_ARG", 2: "RESS_ERR_UNSUPPORTE
 SELECT_MASS, SELECT_DRIFT, SELECT_RANDOM, SELECT_CDF = 0, 1, 2, 3
 DRIFT_MINIMISE, DRIFT_MAXIMISE_SWAPS, DRIFT_MAXIMISE_FULL = 0, 1, 2
 HEAD_DIM, BLOCK = 64, 128
+MAX_TOKEN_DIM = 256
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 
 
 class RessError(RuntimeError):
@@ -43,6 +48,28 @@ class ress_select_params(ctypes.Structure):
                 ("rounds", ctypes.c_int32), ("rho", ctypes.c_float), ("eps", ctypes.c_float),
                 ("seed", ctypes.c_uint64), ("objective", ctypes.c_int32), ("top_p", ctypes.c_float),
                 ("drift", ctypes.c_void_p)]
+
+
+class ress_rope_plan(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("phase", ctypes.c_uint64 * (MAX_TOKEN_DIM // 2))]
+
+
+class ress_rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64), ("stride_t", ctypes.c_int64)]
+
+
+class ress_qk_params(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("tokens", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("norm", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("q_weight", ctypes.c_void_p), ("q_bias", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("k_bias", ctypes.c_void_p),
+                ("rope", ctypes.POINTER(ress_rope_plan)), ("positions", ctypes.c_void_p),
+                ("pos_stride_b", ctypes.c_int64), ("views", ctypes.c_int32),
+                ("specials", ctypes.c_int32)]
 
 
 _lib = None
@@ -75,6 +102,14 @@ _SIGS = {
     "ress_debug_attn_forced_timeout": (_I32, [ctypes.POINTER(ress_shape), _VP, _VP, _VP, _VP,
                                               _VP, ctypes.c_float, _VP, _VP, ctypes.c_int64,
                                               _VP]),
+    "ress_rope_init": (_I32, [ctypes.POINTER(ress_rope_plan), _I32, _I32, _I32, _I32,
+                              ctypes.c_double, _I32, ctypes.c_double, _I32, ctypes.c_double,
+                              ctypes.c_double]),
+    "ress_rope": (_I32, [ctypes.POINTER(ress_rope_plan), _I32, _I32, _I32, _I32,
+                         ctypes.POINTER(ress_rows), _VP, ctypes.c_int64, _I32,
+                         ctypes.POINTER(ress_rows), _VP]),
+    "ress_qk_norm_rope": (_I32, [ctypes.POINTER(ress_qk_params)] + [ctypes.POINTER(ress_rows)] * 6
+                          + [_VP]),
 }
 
 
@@ -272,3 +307,112 @@ def ress_debug_attn_forced_timeout(shape, q, k, v, kv_idx, kv_cnt, scale: float,
                                                _ptr(out), _ptr(dev_err), int(limit_cycles),
                                                _stream(stream))
     _check("ress_debug_attn_forced_timeout", st)
+
+
+# ------------------------------------------------------------------- token operators
+def rope_plan(head_dim: int, rot_dim: Optional[int] = None, axes: int = 1, layout: str = "half",
+              theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+              original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """The rotation of a model (ress_rope_init): computed once, passed to every call.
+    rot_dim: leading elements that are rotated (default: all of head_dim); layout "half" or
+    "interleaved"; scaling "none", "linear", "ntk" or "yarn"."""
+    if layout not in ROPE_LAYOUTS or scaling not in ROPE_SCALINGS:
+        raise ValueError(f"unknown rotary layout {layout!r} or scaling {scaling!r}")
+    plan = ress_rope_plan()
+    st = load().ress_rope_init(ctypes.byref(plan), int(head_dim),
+                               int(head_dim if rot_dim is None else rot_dim), int(axes),
+                               ROPE_LAYOUTS[layout], float(theta), ROPE_SCALINGS[scaling],
+                               float(factor), int(original_len), float(beta_fast),
+                               float(beta_slow))
+    _check("ress_rope_init", st)
+    return plan
+
+
+def _rows(t: torch.Tensor, like=None) -> ress_rows:
+    """A [B, heads, N, D] tensor as strided rows; `like` = (shape, dtype, device) to match."""
+    if t.dim() != 4:
+        raise ValueError("expected a [batch, heads, tokens, head_dim] tensor")
+    if like is not None and (t.shape, t.dtype, t.device) != like:
+        raise ValueError(f"expected {like}, got {(t.shape, t.dtype, t.device)}")
+    b, h, n, e = t.stride()
+    if e != 1 and t.shape[3] > 1:
+        raise ValueError("the elements of a row must be contiguous")
+    return ress_rows(t.data_ptr() or None, b, h, n)
+
+
+def _positions(plan, positions, batch: int, tokens: int, device):
+    """(pointer, batch stride) of int32 positions [tokens], [tokens, axes], [batch or 1, tokens]
+    or [batch or 1, tokens, axes]."""
+    if positions is None:
+        return None, 0
+    if positions.dtype != torch.int32 or positions.device != device:
+        raise ValueError("positions must be int32 on the tensors' device")
+    axes = plan.axes
+    p = positions
+    if axes == 1 and p.dim() <= 2 and (p.dim() == 1 or p.shape[-1] == tokens and p.shape[0] in (1, batch)):
+        p = p.unsqueeze(-1)
+    if p.dim() == 2:
+        p = p.unsqueeze(0)
+    if p.dim() != 3 or p.shape[1:] != (tokens, axes) or p.shape[0] not in (1, batch):
+        raise ValueError(f"positions of shape {tuple(positions.shape)} do not fit "
+                         f"{batch} x {tokens} tokens and {axes} axes")
+    if (axes > 1 and p.stride(2) != 1) or (tokens > 1 and p.stride(1) != axes):
+        raise ValueError("the positions of a batch entry must be contiguous")
+    return p.data_ptr() or None, (p.stride(0) if p.shape[0] > 1 else 0)
+
+
+def _launch(name: str, device, stream, *args):
+    """Calls the library with the tensors' device current, on `stream` or that device's current
+    stream."""
+    if device.type != "cuda":
+        raise ValueError(f"{name} takes CUDA tensors, got {device}")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            st = getattr(load(), name)(*args, _stream(stream))
+    else:
+        st = getattr(load(), name)(*args, _stream(stream))
+    _check(name, st)
+
+
+def ress_rope(plan, x: torch.Tensor, positions: Optional[torch.Tensor], out: torch.Tensor,
+              inverse: bool = False, stream=None):
+    """Rotates x [B, heads, N, D] (any strides over whole rows) into out (may be x)."""
+    if x.shape[-1] != plan.head_dim or x.dtype not in DTYPES:
+        raise ValueError(f"expected rows of {plan.head_dim} bf16, fp16 or fp32 elements")
+    src, dst = _rows(x), _rows(out, (x.shape, x.dtype, x.device))
+    b, h, n, _ = x.shape
+    pos, pos_b = _positions(plan, positions, b, n, x.device)
+    _launch("ress_rope", x.device, stream, ctypes.byref(plan), b, h, n, DTYPES[x.dtype],
+            ctypes.byref(src), pos, pos_b, 1 if inverse else 0, ctypes.byref(dst))
+
+
+def _affine(w: Optional[torch.Tensor], dim: int, device):
+    if w is None:
+        return None
+    if w.dtype != torch.float32 or w.shape != (dim,) or w.device != device:
+        raise ValueError(f"norm weights and biases must be fp32 [{dim}] on the tensors' device")
+    return _ptr(w)
+
+
+def ress_qk_norm_rope(q, k, q_out, k_out, v=None, v_out=None, norm: int = NORM_RMS,
+                      eps: float = 1e-6, q_weight=None, q_bias=None, k_weight=None, k_bias=None,
+                      plan=None, positions=None, views: int = 1, specials: int = 0, stream=None):
+    """Per-head norm and rotation of q and k (and the move of v) in one pass, into the token
+    order of ress_token_gather.  Tensors are [B, heads, N, D] views of any strides."""
+    if q.dim() != 4 or k.dim() != 4 or q.dtype not in DTYPES:
+        raise ValueError("expected [batch, heads, tokens, head_dim] tensors of bf16, fp16 or fp32")
+    if (v is None) != (v_out is None):
+        raise ValueError("v and v_out go together")
+    b, h, n, d = q.shape
+    g = k.shape[1]
+    kv = (torch.Size((b, g, n, d)), q.dtype, q.device)
+    rows = [_rows(q), _rows(k, kv), None if v is None else _rows(v, kv),
+            _rows(q_out, (q.shape, q.dtype, q.device)), _rows(k_out, kv),
+            None if v_out is None else _rows(v_out, kv)]
+    pos, pos_b = (None, 0) if plan is None else _positions(plan, positions, b, n, q.device)
+    aff = [_affine(w, d, q.device) for w in (q_weight, q_bias, k_weight, k_bias)]
+    p = ress_qk_params(b, n, h, g, d, DTYPES[q.dtype], int(norm), float(eps), *aff,
+                       ctypes.pointer(plan) if plan is not None else None, pos, pos_b, int(views),
+                       int(specials))
+    _launch("ress_qk_norm_rope", q.device, stream, ctypes.byref(p),
+            *[None if r is None else ctypes.byref(r) for r in rows])

@@ -14,7 +14,9 @@
  *
  * plus the head Gram matrices M_h that (3) and (4) need (ress_head_gram, computed once
  * per layer at model load) and a longest-first launch order for (5)
- * (ress_attn_schedule).
+ * (ress_attn_schedule).  Around them stand the operators that a layer's queries and keys
+ * go through first, the per-head norm and the rotary positions (ress_qk_norm_rope,
+ * ress_rope).
  *
  * Sources, cited by page title and section / equation:
  *   [ReSS]       "ReSS: Residual-Restoring Sparse Attention for 3D Vision Transformers"
@@ -136,9 +138,11 @@ typedef struct {
                                v_pool, v_bar and gram, and eps > 0.                 */
 } ress_select_params;
 
-/* Version of this ABI (incremented on any change of the exported calls): 5 (version 4:
- * ress_shape gained `key_block`; ress_select_params gained `objective`, `top_p` and
- * `drift`; RESS_SELECT_CDF; version 5: ress_drift_select and its workspace query). */
+/* Version of this ABI (incremented on any change that an earlier caller could meet): 5
+ * (version 4: ress_shape gained `key_block`; ress_select_params gained `objective`, `top_p`
+ * and `drift`; RESS_SELECT_CDF; version 5: ress_drift_select and its workspace query).  The
+ * token operators (ress_rope, ress_qk_norm_rope) were added to version 5; they change no
+ * call or struct that was there. */
 int32_t ress_abi_version(void);
 
 /* Human-readable name of a status code (static string). */
@@ -391,6 +395,126 @@ ress_status ress_debug_attn_forced_timeout(const ress_shape *shape, const void *
                                            const int32_t *kv_idx, const int32_t *kv_cnt,
                                            float scale, void *out, int32_t *dev_err,
                                            int64_t limit_cycles, ress_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Token operators: rotary positions and the per-head norm.  They do not take a ress_shape:
+ * head_dim is 2..256 here, and tensors are strided views, so that the packed output of a
+ * projection is read in place.
+ * ---------------------------------------------------------------------------------- */
+
+typedef enum { RESS_BF16 = 0, RESS_FP16 = 1, RESS_FP32 = 2 } ress_dtype;
+
+/* Which elements of a rotated section of d elements form pair i (i < d/2). */
+typedef enum {
+  RESS_ROPE_HALF = 0,       /* (i, i + d/2)     */
+  RESS_ROPE_INTERLEAVED = 1 /* (2i, 2i + 1)     */
+} ress_rope_layout;
+
+/* How the frequencies theta^(-2i/d) are changed to reach beyond the trained length. */
+typedef enum {
+  RESS_ROPE_PLAIN = 0,
+  RESS_ROPE_LINEAR = 1, /* positions divided by `factor`                                */
+  RESS_ROPE_NTK = 2,    /* theta * factor^(d/(d-2)); d > 2                              */
+  RESS_ROPE_YARN = 3    /* Peng et al., "YaRN" (2023): frequencies of pairs that turn more
+                           than beta_fast times within original_len stay, those that turn
+                           less than beta_slow times are divided by `factor`, with a linear
+                           ramp over the pair index between (its ends are rounded outward to
+                           whole pairs); cosines and sines are multiplied by
+                           0.1 ln(factor) + 1                                            */
+} ress_rope_scaling;
+
+typedef enum { RESS_NORM_NONE = 0, RESS_NORM_RMS = 1, RESS_NORM_LAYER = 2 } ress_norm;
+
+#define RESS_MAX_TOKEN_DIM 256
+
+/* The rotation of a model: filled by ress_rope_init, then constant.  HOST memory, read
+ * during each call (it need not outlive the call). */
+typedef struct {
+  int32_t head_dim; /* elements of a row                                                 */
+  int32_t rot_dim;  /* leading elements that are rotated; the others pass unchanged      */
+  int32_t axes;     /* position axes, 1..3; section a of rot_dim/axes elements turns with
+                       axis a (two axes: the row and column of an image patch)           */
+  int32_t layout;   /* ress_rope_layout, within each section                             */
+  float amplitude;  /* factor of cosine and sine: 1 except for RESS_ROPE_YARN            */
+  int32_t reserved;
+  uint64_t phase[RESS_MAX_TOKEN_DIM / 2]; /* turns per position of pair i of a section, as
+                       a fraction of 2^64 */
+} ress_rope_plan;
+
+/*
+ * ress_rope_init -- fills *plan (host arithmetic only).
+ *   head_dim 2..256; rot_dim even multiple of axes (rot_dim/axes even), 2..head_dim;
+ *   theta > 1, at most 1e12; scaling: ress_rope_scaling; factor 1..1e6 (ignored for
+ *   PLAIN); original_len >= 1 and 0 < beta_slow < beta_fast (YARN only; usually 1 and 32).
+ * Errors: INVALID_ARG.
+ */
+ress_status ress_rope_init(ress_rope_plan *plan, int32_t head_dim, int32_t rot_dim, int32_t axes,
+                           int32_t layout, double theta, int32_t scaling, double factor,
+                           int32_t original_len, double beta_fast, double beta_slow);
+
+/* A strided view of rows: element (b, h, t, e) is at ptr[b*stride_b + h*stride_h +
+ * t*stride_t + e].  Strides in elements, >= 0.  ptr needs the alignment of its element
+ * type; views whose every row starts on a 16-byte boundary take a faster kernel. */
+typedef struct {
+  void *ptr; /* DEVICE; read only where the view is an input */
+  int64_t stride_b, stride_h, stride_t;
+} ress_rows;
+
+/*
+ * ress_rope -- rotates rows by their positions: pair (x_a, x_b) of section s becomes
+ *   A (x_a cos w - x_b sin w, x_b cos w + x_a sin w),   w = position[s] * frequency,
+ * A the plan's amplitude.  inverse = 1 turns by -w (the transposed map: the gradient of the
+ * forward call, and its inverse where A = 1).  fp32 arithmetic from the stored type,
+ * rounded once.  w is reduced exactly: an angle is as precise at position 2^30 as at 1.
+ *   batch, heads, tokens >= 0: x and out are [batch, heads, tokens, plan->head_dim].
+ *   dtype: ress_dtype of x and out.
+ *   positions  DEVICE int32 [batch or 1][tokens][axes], any sign, 4-byte aligned;
+ *              pos_stride_b: elements from one batch entry's to the next (0: shared).
+ *              NULL (axes = 1 only): a token's position is its index.
+ *   out        may be x itself (same pointer and strides).  Otherwise the two must not
+ *              overlap, and rows of out must not overlap one another (INVALID_ARG where a
+ *              stride is too small for that).
+ */
+ress_status ress_rope(const ress_rope_plan *plan, int32_t batch, int32_t heads, int32_t tokens,
+                      int32_t dtype, const ress_rows *x, const int32_t *positions,
+                      int64_t pos_stride_b, int32_t inverse, const ress_rows *out,
+                      ress_stream_t stream);
+
+typedef struct {
+  int32_t batch, tokens;       /* >= 0 */
+  int32_t q_heads, kv_heads;   /* >= 1 */
+  int32_t head_dim;            /* 2..256 */
+  int32_t dtype;               /* ress_dtype of every tensor */
+  int32_t norm;                /* ress_norm, over the head_dim elements of each row */
+  float eps;                   /* >= 0 */
+  const float *q_weight, *q_bias, *k_weight, *k_bias; /* DEVICE fp32 [head_dim], or NULL
+                                  (weight 1, bias 0); used only with a norm */
+  const ress_rope_plan *rope;  /* HOST, or NULL: no rotation; its head_dim must be this one */
+  const int32_t *positions;    /* as for ress_rope, by the token's place in the input */
+  int64_t pos_stride_b;
+  int32_t views, specials;     /* >= 1, >= 0: the token order of ress_token_gather (inverse
+                                  = 0) for the outputs; views = 1 with specials = 0 keeps it */
+} ress_qk_params;
+
+/*
+ * ress_qk_norm_rope -- what a layer does to its projection's queries and keys before
+ * attention, in one pass: each (token, head) row of q and k is normalised over its head_dim
+ * elements
+ *   RMS:   x / sqrt(mean(x^2) + eps) * weight + bias
+ *   LAYER: (x - mean) / sqrt(mean((x - mean)^2) + eps) * weight + bias
+ * and then rotated as by ress_rope; v, if given, is copied.  All three are written in the
+ * token order of ress_token_gather, so that packed [B,N,3,H,64] projections become the
+ * [B,H,N,64] tensors of the calls above without further passes.  fp32 arithmetic, rounded
+ * once (a row whose sum of squares passes the fp32 range overflows as in that arithmetic).
+ *   q, q_out [batch, q_heads, tokens, head_dim]; k, v and k_out, v_out with kv_heads.
+ *   v, v_out: both or neither NULL.
+ *   In place (an output that is its input, same pointer and strides) is allowed where the
+ *   token order is kept.  Otherwise outputs overlap neither inputs nor one another.
+ */
+ress_status ress_qk_norm_rope(const ress_qk_params *params, const ress_rows *q,
+                              const ress_rows *k, const ress_rows *v, const ress_rows *q_out,
+                              const ress_rows *k_out, const ress_rows *v_out,
+                              ress_stream_t stream);
 
 #ifdef __cplusplus
 }
