@@ -13,7 +13,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libress.so")
-SOURCES = ["ress_api.cu", "k_blocks.cu", "k_select.cu", "k_attn.cu", "k_rope.cu"]
+SOURCES = ["ress_api.cu", "k_blocks.cu", "k_select.cu", "k_attn.cu", "k_masked_attn.cu",
+           "k_rope.cu"]
 HEADERS = ["ress_common.cuh", "ress_internal.h", "k_tiles.cuh", "k_topk.cuh",
            "k_attn.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

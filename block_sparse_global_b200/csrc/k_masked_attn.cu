@@ -1,0 +1,806 @@
+// Attention over kept key blocks with changed scores: capped by a tanh, lowered with the
+// distance of the positions, masked by document and by order (sm_100a, tcgen05).
+//
+// Mathematics, per query t of a head and key u of a kept block (log2 domain):
+//   z = C tanh(scale s / c)          C = c log2 e, or scale log2 e * s without a cap
+//   z = z - slope log2 e |pos_t - pos_u|
+//   z = -inf  unless doc_t = doc_u >= 0 and order_u <= order_t
+//   m = max z,  l = sum 2^(z - m),  out = sum 2^(z - m) v / l,  lse = ln 2 (m + log2 l)
+// with the running m and l of an online softmax in fp32, and products of bf16 operands
+// accumulated in fp32 by the tensor cores.  P is rounded to bf16 for the second product; l
+// sums the unrounded values.
+//
+// Work split.  One CTA per (batch, head, query block of 128) row; two CTAs share an SM.  A
+// CTA first walks its list of kept blocks against the blocks' summaries (smallest and
+// largest document and order, one int4 per key block, written by summary_kernel) and keeps
+// in shared memory the blocks that some query of the row sees, each marked whole (every
+// pair visible) or partial.  Blocks that nobody sees cost no load and no product; whole
+// blocks take no per-element test.  When the rows are few, `splits` CTAs share a row: each
+// takes a contiguous part of its tiles and writes its unnormalised sums, and join_kernel
+// weighs them together.
+//
+// Warp roles are those of k_attn.cu (192 threads): warps 0-3 softmax, one query row per
+// thread; warp 4 the TMA producer; warp 5 the tensor-core issuer.  Tensor memory: S columns
+// [0,128), P [128,192), O [192,256).
+//
+// Masked values.  P of a masked pair is exactly 0, but 0 times an infinite or NaN value is
+// NaN inside the matrix product.  In partial tiles of a masked call the softmax warps
+// therefore look at the tile's values: if one is not finite, it is added by hand to the
+// rows that see its token, and replaced by 0 in shared memory before the product.
+#include <algorithm>
+#include <climits>
+
+#include "k_attn.cuh"
+#include "ress_internal.h"
+
+namespace ress {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kWarps = kThreads / 32;
+constexpr int kProducerWarp = 4;
+constexpr int kMmaWarp = 5;
+constexpr float kRescaleLog2 = 8.0f;  // O and l are rescaled when the max grows by more
+constexpr float kNoMax = -3.0e38f;    // running max of a row that has seen no key
+constexpr int kKStages = 3;
+constexpr int kVStages = 2;
+constexpr int kTile = 128 * 64 * 2;  // bytes of one 128 x 64 bf16 tile
+constexpr int kOffQ = 0;
+constexpr int kOffK = kTile;
+constexpr int kOffV = kOffK + kKStages * kTile;
+constexpr int kOffList = kOffV + kVStages * kTile;         // uint16 per kept block
+constexpr int kOffMeta = kOffList + 2 * kMaxBlocks;        // per softmax warp: doc, order, pos
+constexpr int kOffBar = kOffMeta + 4 * 3 * 128 * 4;
+constexpr int kSmemBytes = kOffBar + 384 + 1024;
+static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+constexpr uint32_t kTmemCols = 256;
+constexpr uint32_t kColS = 0, kColP = 128, kColO = 192;
+constexpr uint16_t kPartial = 0x8000;  // list entry: block index, and this if not whole
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+struct Bars {
+  uint64_t q_full;
+  uint64_t k_full[kKStages];
+  uint64_t k_empty[kKStages];
+  uint64_t v_full[kVStages];
+  uint64_t v_empty[kVStages];
+  uint64_t s_full;
+  uint64_t s_free;
+  uint64_t p_full;
+  uint64_t o_done;
+  uint64_t o_half;
+  uint64_t drain;
+  uint64_t scan;  // the softmax warps' look at a partial tile's values
+  uint32_t tmem_base;
+  int abort;
+  int o_init;           // O was started by hand: the first product adds to it
+  int count[kWarps];    // filter: visible blocks of each warp's entries
+  int qsum[4][5];       // filter: each softmax warp's query summary
+  uint32_t vflag[2][4];  // rows of V (32 per word) that hold a value that is not finite
+};
+static_assert(sizeof(Bars) <= 384, "barriers fit their shared-memory slot");
+
+RESS_DEV float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// A wait of a whole warp: every lane sees the same answer, so that a warp that gives up
+// leaves its loop together.
+RESS_DEV bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+RESS_DEV void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// tanh(y) = 1 - 2 / (1 + e^2y) has an absolute error of an fp32 unit; below 1/2 the odd
+// series keeps the relative one (terms to y^13; the next is below 1e-7 of the sum at 1/2).
+RESS_DEV float tanh_small(float y) {
+  const float y2 = y * y;
+  float t = 21844.0f / 6081075.0f;
+  t = fmaf(t, y2, -1382.0f / 155925.0f);
+  t = fmaf(t, y2, 62.0f / 2835.0f);
+  t = fmaf(t, y2, -17.0f / 315.0f);
+  t = fmaf(t, y2, 2.0f / 15.0f);
+  t = fmaf(t, y2, -1.0f / 3.0f);
+  return fmaf(t * y2, y, y);
+}
+RESS_DEV float tanh_full(float y) {
+  const float r = rcp_approx(1.0f + ex2_approx(2.0f * kLog2e * y));
+  return fabsf(y) < 0.5f ? tanh_small(y) : fmaf(-2.0f, r, 1.0f);
+}
+
+struct Params {
+  const int32_t *kv_idx, *kv_cnt, *order;
+  const int32_t *q_pos, *k_pos, *q_doc, *k_doc, *q_order, *k_order;
+  const float *slopes;
+  const int4 *blocks;  // [B][nk]: smallest and largest document, smallest and largest order
+  __nv_bfloat16 *out;
+  float *lse;
+  float *part_o;    // [items][splits][128][64]
+  float2 *part_ml;  // [items][splits][128]
+  int32_t *dev_err;
+  int H, N, Nq, nq, nk;
+  int splits;
+  float scale_log2;         // without a cap
+  float cap_log2, cap_in;   // c log2 e; scale / c
+};
+
+// KB tokens per key block; CAP, BIAS: the score changes compiled in.
+template <int KB, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 2)
+    masked_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = reinterpret_cast<unsigned char *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Bars *bar = reinterpret_cast<Bars *>(smem + kOffBar);
+  uint16_t *list = reinterpret_cast<uint16_t *>(smem + kOffList);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // rows of a head from its last query block to its first: under an order mask the long
+  // rows start first, and a head's keys stay in L2 while its rows run
+  const long long x = blockIdx.x;
+  const long long item = p.order ? (long long)p.order[x] : x / p.nq * p.nq + (p.nq - 1 - (int)(x % p.nq));
+  const long long bh = item / p.nq;
+  const int qi = (int)(item - bh * p.nq);
+  const int b = (int)(bh / p.H), h = (int)(bh - (long long)b * p.H);
+  const bool masked = p.q_doc != nullptr || p.q_order != nullptr;
+
+  // softmax warps that hold a query (the others stay out: their rows of S, P and O are
+  // never read)
+  const int active = min(4, (p.Nq - qi * 128 + 31) >> 5);
+
+  if (tid == 0) {
+    mbar_init(&bar->q_full, 1);
+    for (int s = 0; s < kKStages; ++s) {
+      mbar_init(&bar->k_full[s], 1);
+      mbar_init(&bar->k_empty[s], 1);
+    }
+    for (int s = 0; s < kVStages; ++s) {
+      mbar_init(&bar->v_full[s], 1);
+      mbar_init(&bar->v_empty[s], 1);
+    }
+    mbar_init(&bar->s_full, 1);
+    mbar_init(&bar->s_free, active);
+    mbar_init(&bar->p_full, active);
+    mbar_init(&bar->o_done, 1);
+    mbar_init(&bar->o_half, 1);
+    mbar_init(&bar->drain, 1);
+    mbar_init(&bar->scan, active);
+    bar->abort = 0;
+    bar->o_init = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bar->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+
+  // ---------------------------------------------------------------- the row's blocks
+  const int t = qi * 128 + tid;  // query token of a softmax thread
+  int row_doc = 0, row_order = 0;
+  if (warp < 4) {
+    const bool there = t < p.Nq;
+    if (p.q_doc) row_doc = there ? p.q_doc[(long long)b * p.Nq + t] : -1;
+    if (p.q_order) row_order = there ? p.q_order[(long long)b * p.Nq + t] : 0;
+    // over the rows that may see something: documents, orders, and whether some see nothing
+    const bool live = there && row_doc >= 0;
+    int v[5] = {live ? row_doc : INT_MAX, live ? row_doc : INT_MIN, live ? row_order : INT_MAX,
+                live ? row_order : INT_MIN, there && row_doc < 0};
+    v[0] = __reduce_min_sync(0xffffffffu, v[0]);
+    v[1] = __reduce_max_sync(0xffffffffu, v[1]);
+    v[2] = __reduce_min_sync(0xffffffffu, v[2]);
+    v[3] = __reduce_max_sync(0xffffffffu, v[3]);
+    v[4] = __reduce_or_sync(0xffffffffu, v[4]);
+    if (lane == 0)
+      for (int i = 0; i < 5; ++i) bar->qsum[warp][i] = v[i];
+    if (row_doc < 0) row_doc = -2;  // equal to no key's document
+  }
+  __syncthreads();
+  int q_dmin = INT_MAX, q_dmax = INT_MIN, q_omin = INT_MAX, q_omax = INT_MIN, q_dead = 0;
+  for (int w = 0; w < 4; ++w) {
+    q_dmin = min(q_dmin, bar->qsum[w][0]);
+    q_dmax = max(q_dmax, bar->qsum[w][1]);
+    q_omin = min(q_omin, bar->qsum[w][2]);
+    q_omax = max(q_omax, bar->qsum[w][3]);
+    q_dead |= bar->qsum[w][4];
+  }
+  const int cnt = p.kv_cnt ? p.kv_cnt[item] : p.nk;
+  const int32_t *kvrow = p.kv_idx ? p.kv_idx + item * p.nk : nullptr;
+  const bool ragged = p.N % KB != 0;
+  bool bad = cnt < 0 || cnt > p.nk;
+  int kept = 0;
+  if (!bad) {
+    for (int j0 = 0; j0 < cnt; j0 += kThreads) {
+      const int j = j0 + tid;
+      int kb = -1;
+      bool see = false, whole = true;
+      if (j < cnt) {
+        kb = kvrow ? kvrow[j] : j;
+        if (kb < 0 || kb >= p.nk) {
+          bad = true;
+        } else {
+          see = true;
+          if (masked) {
+            const int4 s = p.blocks[(long long)b * p.nk + kb];
+            if (p.q_doc) {
+              see = q_dmax >= 0 && s.y >= 0 && max(s.x, 0) <= q_dmax && s.y >= q_dmin;
+              whole = !q_dead && q_dmin == q_dmax && s.x == s.y && s.x == q_dmin;
+            }
+            if (p.q_order) {
+              see = see && s.z <= q_omax;
+              whole = whole && s.w <= q_omin;
+            }
+          }
+          if (ragged && kb == p.nk - 1) whole = false;
+        }
+      }
+      const uint32_t seen = __ballot_sync(0xffffffffu, see);
+      if (lane == 0) bar->count[warp] = __popc(seen);
+      __syncthreads();
+      int at = kept;
+      for (int w = 0; w < kWarps; ++w) {
+        const int n = bar->count[w];
+        if (w < warp) at += n;
+        kept += n;
+      }
+      if (see) list[at + __popc(seen & ((1u << lane) - 1))] = (uint16_t)kb | (whole ? 0 : kPartial);
+      __syncthreads();
+    }
+  }
+  tc_fence_before();
+  const int any_bad = __syncthreads_or(bad);
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem_base;
+  volatile int *abort = &bar->abort;
+  // this CTA's tiles of the row
+  const int all_tiles = KB == 128 ? kept : (kept + 1) >> 1;
+  const int first = (int)((long long)all_tiles * blockIdx.y / p.splits);
+  const int tiles = any_bad ? 0 : (int)((long long)all_tiles * (blockIdx.y + 1) / p.splits) - first;
+  if (any_bad && tid == 0) report_error(p.dev_err, RESS_ERR_DEVICE_BOUNDS);
+  // partial sums of a shared row
+  const long long slot = item * p.splits + blockIdx.y;
+
+  if (tiles > 0) {
+    const int entries = KB == 128 ? tiles : min(2 * tiles, kept - 2 * first);
+    const uint16_t *mine = list + (KB == 128 ? first : 2 * first);
+    if (warp == kProducerWarp) {
+      // ------------------------------------------------------------ TMA producer
+      if (lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+        mbar_arrive_expect_tx(&bar->q_full, kTile);
+        tma_load_3d(smem + kOffQ, &tmQ, &bar->q_full, 0, qi * 128, (int)bh);
+        // one 128-row box, or two 64-row boxes (row N, past the last token, reads as zero
+        // where the row has no second block)
+        auto load_tile = [&](const CUtensorMap *tm, unsigned char *dst, uint64_t *full, int j) {
+          mbar_arrive_expect_tx(full, kTile);
+          if constexpr (KB == 128) {
+            tma_load_3d(dst, tm, full, 0, (mine[j] & ~kPartial) * 128, (int)bh);
+          } else {
+            const int r1 = 2 * j + 1 < entries ? (mine[2 * j + 1] & ~kPartial) * 64 : p.N;
+            tma_load_3d(dst, tm, full, 0, (mine[2 * j] & ~kPartial) * 64, (int)bh);
+            tma_load_3d(dst + kTile / 2, tm, full, 0, r1, (int)bh);
+          }
+        };
+        auto load_k = [&](int j) {
+          const int s = j % kKStages;
+          load_tile(&tmK, smem + kOffK + s * kTile, &bar->k_full[s], j);
+        };
+        auto load_v = [&](int j) {
+          const int s = j % kVStages;
+          load_tile(&tmV, smem + kOffV + s * kTile, &bar->v_full[s], j);
+        };
+        int nk = min(tiles, kKStages), nv = min(tiles, kVStages);
+        for (int j = 0; j < nk; ++j) load_k(j);
+        for (int j = 0; j < nv; ++j) load_v(j);
+        for (int j = 0; j < tiles; ++j) {
+          if (j + kKStages < tiles) {
+            if (!mbar_wait(&bar->k_empty[j % kKStages], (j / kKStages) & 1, abort)) break;
+            load_k(j + kKStages);
+            nk = j + kKStages + 1;
+          }
+          if (j + kVStages < tiles) {
+            if (!mbar_wait(&bar->v_empty[j % kVStages], (j / kVStages) & 1, abort)) break;
+            load_v(j + kVStages);
+            nv = j + kVStages + 1;
+          }
+        }
+        if (*abort == 0 && (nk < tiles || nv < tiles)) {
+          report_error(p.dev_err, RESS_ERR_DEVICE_TIMEOUT);
+          *abort = 1;
+        }
+        // never leave the CTA with copies in flight
+        for (int j = max(0, nk - kKStages); j < nk; ++j)
+          mbar_wait(&bar->k_full[j % kKStages], (j / kKStages) & 1, nullptr);
+        for (int j = max(0, nv - kVStages); j < nv; ++j)
+          mbar_wait(&bar->v_full[j % kVStages], (j / kVStages) & 1, nullptr);
+        mbar_wait(&bar->q_full, 0, nullptr);
+      }
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------ tensor-core issuer
+      if (lane == 0) {
+        const uint32_t sQ = smem_u32(smem + kOffQ);
+        const uint32_t sK = smem_u32(smem + kOffK);
+        const uint32_t sV = smem_u32(smem + kOffV);
+        volatile int *o_init = &bar->o_init;
+        bool ok = mbar_wait(&bar->q_full, 0, abort);
+        tc_fence_after();
+        const uint64_t dq = smem_desc(sQ);
+        for (int j = 0; ok && j <= tiles; ++j) {
+          if (j < tiles) {
+            const int s = j % kKStages;
+            ok = mbar_wait(&bar->k_full[s], (j / kKStages) & 1, abort);
+            if (ok && j > 0) ok = mbar_wait(&bar->s_free, (j - 1) & 1, abort);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dk = smem_desc(sK + s * kTile);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_ss(tmem + kColS, dq + 2 * k, dk + 2 * k, kIdescS, k > 0);
+            mma_commit(&bar->s_full);
+            mma_commit(&bar->k_empty[s]);
+          }
+          if (j > 0) {
+            const int jp = j - 1, sp = jp % kVStages;
+            ok = mbar_wait(&bar->p_full, jp & 1, abort);
+            if (ok) ok = mbar_wait(&bar->v_full[sp], (jp / kVStages) & 1, abort);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dv = smem_desc(sV + sp * kTile);
+            const bool add = jp > 0 || *o_init != 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              mma_ts(tmem + kColO, tmem + kColP + 8 * k, dv + 128 * k, kIdescPV, (add || k > 0));
+              if (k == 3) mma_commit(&bar->o_half);
+            }
+            mma_commit(&bar->o_done);
+            mma_commit(&bar->v_empty[sp]);
+          }
+        }
+        if (!ok) {
+          report_error(p.dev_err, RESS_ERR_DEVICE_TIMEOUT);
+          *abort = 1;
+        }
+        // drain: every MMA issued above has finished before the CTA tears down
+        mma_commit(&bar->drain);
+        mbar_wait(&bar->drain, 0, nullptr);
+      }
+    } else if (warp < active) {
+      // ------------------------------------------------------------- softmax
+      const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
+      int *m_doc = reinterpret_cast<int *>(smem + kOffMeta) + warp * 3 * 128;
+      int *m_order = m_doc + 128;
+      float *m_pos = reinterpret_cast<float *>(m_doc + 256);
+      float row_pos = 0.f, slope = 0.f;
+      if constexpr (BIAS) {
+        row_pos = t < p.Nq ? (float)p.q_pos[(long long)b * p.Nq + t] : 0.f;
+        slope = -p.slopes[h] * kLog2e;
+      }
+      float m_run = kNoMax, l_run = 0.f;
+      bool ok = true;
+      int scans = 0, scan_phase = 0;
+      for (int j = 0; j < tiles && ok; ++j) {
+        const int e0 = KB == 128 ? mine[j] : mine[2 * j];
+        const int e1 = KB == 128 ? e0 : (2 * j + 1 < entries ? mine[2 * j + 1] : -1);
+        const bool partial = ((e0 | e1) & kPartial) != 0;  // an absent block (-1) is partial
+        // key of column c, or -1
+        auto key_of = [&](int c) {
+          int u;
+          if constexpr (KB == 128) {
+            u = (e0 & ~kPartial) * 128 + c;
+          } else {
+            if (c >= 64 && e1 < 0) return -1;
+            u = ((c < 64 ? e0 : e1) & 0x7fff) * 64 + (c & 63);
+          }
+          return u < p.N ? u : -1;
+        };
+        if (BIAS || partial) {
+          __syncwarp();  // the last tile's values have been read
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = lane + 32 * i, u = key_of(c);
+            const long long at = (long long)b * p.N + u;
+            if constexpr (BIAS) m_pos[c] = u >= 0 ? (float)__ldg(p.k_pos + at) : 0.f;
+            if (partial) {
+              m_doc[c] = u < 0 ? -1 : (p.k_doc ? max(__ldg(p.k_doc + at), -1) : 0);
+              m_order[c] = u < 0 || !p.k_order ? 0 : __ldg(p.k_order + at);
+            }
+          }
+          __syncwarp();
+        }
+        ok = warp_wait(&bar->s_full, j & 1, abort);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sv[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          tmem_ld32(trow + kColS + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * i]));
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->s_free);
+        if constexpr (CAP) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            sv[c] = __float_as_uint(p.cap_log2 * tanh_full(__uint_as_float(sv[c]) * p.cap_in));
+        }
+        if constexpr (BIAS) {
+#pragma unroll
+          for (int c = 0; c < 128; c += 4) {
+            const float4 kp = *reinterpret_cast<const float4 *>(m_pos + c);
+            const float d[4] = {fabsf(row_pos - kp.x), fabsf(row_pos - kp.y), fabsf(row_pos - kp.z),
+                                fabsf(row_pos - kp.w)};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float z = CAP ? __uint_as_float(sv[c + i]) : __uint_as_float(sv[c + i]) * p.scale_log2;
+              sv[c + i] = __float_as_uint(fmaf(slope, d[i], z));
+            }
+          }
+        }
+        if (partial) {
+#pragma unroll
+          for (int c = 0; c < 128; c += 4) {
+            const int4 kd = *reinterpret_cast<const int4 *>(m_doc + c);
+            const int4 ko = *reinterpret_cast<const int4 *>(m_order + c);
+            if (kd.x != row_doc || ko.x > row_order) sv[c] = __float_as_uint(-INFINITY);
+            if (kd.y != row_doc || ko.y > row_order) sv[c + 1] = __float_as_uint(-INFINITY);
+            if (kd.z != row_doc || ko.z > row_order) sv[c + 2] = __float_as_uint(-INFINITY);
+            if (kd.w != row_doc || ko.w > row_order) sv[c + 3] = __float_as_uint(-INFINITY);
+          }
+        }
+        // values of a partial tile that are not finite: which rows of V hold one
+        uint32_t vbad[4] = {0, 0, 0, 0};
+        const int sp = j % kVStages;
+        const bool scan = masked && partial;
+        if (scan) {
+          ok = warp_wait(&bar->v_full[sp], (j / kVStages) & 1, abort);
+          if (!ok) break;
+          for (int r = warp; r < 4; r += active) {
+            const uint4 *vr = reinterpret_cast<const uint4 *>(smem + kOffV + sp * kTile + (32 * r + lane) * 128);
+            bool inf = false;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 w = vr[(i + lane) & 7];
+              for (uint32_t y : {w.x, w.y, w.z, w.w})
+                inf |= (y & 0x7f80u) == 0x7f80u || (y & 0x7f800000u) == 0x7f800000u;
+            }
+            const uint32_t bits = __ballot_sync(0xffffffffu, inf);
+            if (lane == 0) *reinterpret_cast<volatile uint32_t *>(&bar->vflag[scans & 1][r]) = bits;
+          }
+          if (lane == 0) mbar_arrive(&bar->scan);
+          ok = warp_wait(&bar->scan, scan_phase & 1, abort);
+          if (!ok) break;
+          ++scan_phase;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vbad[i] = *reinterpret_cast<volatile uint32_t *>(&bar->vflag[scans & 1][i]);
+          ++scans;
+        }
+        const bool by_hand = (vbad[0] | vbad[1] | vbad[2] | vbad[3]) != 0;
+        // row max
+        float mc[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mc[q] = fmaxf(__uint_as_float(sv[2 * q]), __uint_as_float(sv[2 * q + 1]));
+#pragma unroll
+        for (int c = 8; c < 128; c += 8) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            mc[q] = fmax3(mc[q], __uint_as_float(sv[c + 2 * q]), __uint_as_float(sv[c + 2 * q + 1]));
+        }
+        const float sc = CAP || BIAS ? 1.0f : p.scale_log2;
+        const float mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
+        const float m_new = fmaxf(m_run, mx * sc);
+        const bool rescale = m_new > m_run + kRescaleLog2;
+        const float m_use = rescale ? m_new : m_run;
+        const float alpha = rescale ? ex2_approx(m_run - m_new) : 1.0f;
+        const uint64_t sc2 = f2(sc, sc);
+        const uint64_t nm2 = f2(-m_use, -m_use);
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+        uint32_t pk[64];
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+          const uint64_t s2 = f2(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1]));
+          const uint64_t z = CAP || BIAS ? fadd2(s2, nm2) : ffma2(s2, sc2, nm2);
+          const uint64_t e = f2(ex2_approx(f2lo(z)), ex2_approx(f2hi(z)));
+          acc[c & 3] = fadd2(acc[c & 3], e);
+          pk[c] = pack_bf16x2(f2lo(e), f2hi(e));
+          if (c == 31) {
+            // keys 0..63 of P: free once the first half of the previous product is done
+            if (j > 0) ok = warp_wait(&bar->o_half, (j - 1) & 1, abort);
+            if (ok) tmem_st32(trow + kColP, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+          }
+        }
+        if (!ok) break;
+        const uint64_t a = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+        l_run = l_run * alpha + (f2lo(a) + f2hi(a));
+        if (j > 0) {
+          ok = warp_wait(&bar->o_done, (j - 1) & 1, abort);
+          if (!ok) break;
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, rescale)) {
+            uint32_t ov[32];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              tmem_ld32(trow + kColO + 32 * i, ov);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha);
+              tmem_st32(trow + kColO + 32 * i, ov);
+            }
+          }
+        }
+        tmem_st32(trow + kColP + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+        tmem_wait_st();
+        if (by_hand) {
+          // values that are not finite go to the rows that see them, and out of the tile
+          unsigned char *vt = smem + kOffV + sp * kTile;
+          uint32_t ov[32];
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i) {
+            if (j > 0) {
+              tmem_ld32(trow + kColO + 32 * i, ov);
+              tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) ov[c] = 0;
+            }
+#pragma unroll 1
+            for (int u = 0; u < 128; ++u) {
+              const uint32_t word = u < 32 ? vbad[0] : (u < 64 ? vbad[1] : (u < 96 ? vbad[2] : vbad[3]));
+              if (!(word >> (u & 31) & 1) || m_doc[u] != row_doc || m_order[u] > row_order) continue;
+#pragma unroll
+              for (int c = 0; c < 32; ++c) {
+                const int d = 32 * i + c;
+                const uint32_t bits = *reinterpret_cast<const uint16_t *>(
+                    vt + u * 128 + (((d >> 3) ^ (u & 7)) << 4) + (d & 7) * 2);
+                if ((bits & 0x7f80u) == 0x7f80u)
+                  ov[c] = __float_as_uint(__uint_as_float(ov[c]) + __uint_as_float(bits << 16));
+              }
+            }
+            __syncwarp();
+            tmem_st32(trow + kColO + 32 * i, ov);
+          }
+          tmem_wait_st();
+          if (lane == 0) {
+            if (j == 0) *reinterpret_cast<volatile int *>(&bar->o_init) = 1;
+            mbar_arrive(&bar->scan);
+          }
+          ok = warp_wait(&bar->scan, scan_phase & 1, abort);
+          if (!ok) break;
+          ++scan_phase;
+          for (int r = warp; r < 4; r += active) {
+            uint16_t *vr = reinterpret_cast<uint16_t *>(vt + (32 * r + lane) * 128);
+#pragma unroll 1
+            for (int c = 0; c < 64; ++c)
+              if ((vr[c] & 0x7f80u) == 0x7f80u) vr[c] = 0;
+          }
+          fence_async_shared();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->p_full);
+        m_run = m_use;
+      }
+      if (ok) ok = warp_wait(&bar->o_done, (tiles - 1) & 1, abort);
+      if (!ok) {
+        report_error(p.dev_err, RESS_ERR_DEVICE_TIMEOUT);
+        *abort = 1;
+        if (p.splits > 1 && t < p.Nq) p.part_ml[slot * 128 + tid] = make_float2(0.f, -1.f);
+      } else {
+        tc_fence_after();
+        uint32_t o[64];
+        tmem_ld32(trow + kColO, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
+        tmem_ld32(trow + kColO + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
+        tmem_wait_ld();
+        if (t < p.Nq && p.splits > 1) {
+          p.part_ml[slot * 128 + tid] = make_float2(m_run, l_run);
+          uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + (slot * 128 + tid) * 64);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        } else if (t < p.Nq) {
+          // a row that saw no key is zero whatever the products hold
+          const bool none = l_run == 0.f;
+          const float inv = 1.0f / l_run;
+          uint32_t w[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            w[c] = none ? 0u : pack_bf16x2(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv);
+          uint4 *dst = reinterpret_cast<uint4 *>(p.out + ((size_t)bh * p.Nq + t) * 64);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) dst[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+          if (p.lse)
+            p.lse[(size_t)bh * p.Nq + t] = none ? -INFINITY : (m_run + __log2f(l_run)) * kLn2;
+        }
+      }
+    }
+  } else if (warp < 4 && t < p.Nq) {
+    if (p.splits > 1) {
+      p.part_ml[slot * 128 + tid] = make_float2(kNoMax, any_bad ? -1.f : 0.f);
+    } else if (!any_bad) {
+      // nothing to see: zero rows
+      uint4 *dst = reinterpret_cast<uint4 *>(p.out + ((size_t)bh * p.Nq + t) * 64);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
+      if (p.lse) p.lse[(size_t)bh * p.Nq + t] = -INFINITY;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// ------------------------------------------------------------------------ join
+// One warp per query row: out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.  A split with
+// l = 0 saw no key (its O is not written); one with l < 0 met an error and leaves the row
+// as it was.
+__global__ void __launch_bounds__(256) join_kernel(const float *__restrict__ part_o,
+                                                   const float2 *__restrict__ part_ml, int splits, int nq,
+                                                   int Nq, long long rows, __nv_bfloat16 *__restrict__ out,
+                                                   float *__restrict__ lse) {
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  const long long bh = row / Nq;
+  const int t = (int)(row - bh * Nq);
+  const long long slot0 = (bh * nq + (t >> 7)) * splits;
+  const int r = t & 127;
+  float m = kNoMax;
+  bool bad = false;
+  for (int s = lane; s < splits; s += 32) {
+    const float2 ml = part_ml[(slot0 + s) * 128 + r];
+    m = fmaxf(m, ml.x);
+    bad |= ml.y < 0.f;
+  }
+  if (__any_sync(0xffffffffu, bad)) return;
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float l = 0.f, o0 = 0.f, o1 = 0.f;
+  for (int s = 0; s < splits; ++s) {
+    const float2 ml = part_ml[(slot0 + s) * 128 + r];
+    if (ml.y == 0.f) continue;
+    const float w = ex2_approx(ml.x - m);
+    const float2 v = *reinterpret_cast<const float2 *>(part_o + ((slot0 + s) * 128 + r) * 64 + 2 * lane);
+    l += w * ml.y;
+    o0 += w * v.x;
+    o1 += w * v.y;
+  }
+  const bool none = l == 0.f;
+  const float inv = 1.0f / l;
+  reinterpret_cast<uint32_t *>(out + row * 64)[lane] = none ? 0u : pack_bf16x2(o0 * inv, o1 * inv);
+  if (lse && lane == 0) lse[row] = none ? -INFINITY : (m + __log2f(l)) * kLn2;
+}
+
+// ------------------------------------------------------------------- block summaries
+// One warp per key block: {min doc, max doc, min order, max order} over its tokens.
+__global__ void __launch_bounds__(256) summary_kernel(const int32_t *__restrict__ doc,
+                                                      const int32_t *__restrict__ order, int N, int nk,
+                                                      int kb, long long blocks, int4 *__restrict__ out) {
+  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (i >= blocks) return;
+  const long long b = i / nk;
+  const int j = (int)(i - b * nk);
+  int4 s = make_int4(INT_MAX, INT_MIN, INT_MAX, INT_MIN);
+  for (int u = j * kb + lane; u < min(N, (j + 1) * kb); u += 32) {
+    const int d = doc ? doc[b * N + u] : 0, o = order ? order[b * N + u] : 0;
+    s.x = min(s.x, d);
+    s.y = max(s.y, d);
+    s.z = min(s.z, o);
+    s.w = max(s.w, o);
+  }
+  s.x = __reduce_min_sync(0xffffffffu, s.x);
+  s.y = __reduce_max_sync(0xffffffffu, s.y);
+  s.z = __reduce_min_sync(0xffffffffu, s.z);
+  s.w = __reduce_max_sync(0xffffffffu, s.w);
+  if (lane == 0) out[i] = s;
+}
+
+// Rows of a problem without keys: zero, and lse = -inf.
+__global__ void __launch_bounds__(256) no_keys_kernel(long long rows, uint4 *__restrict__ out,
+                                                      float *__restrict__ lse) {
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < rows * 8; i += (long long)gridDim.x * 256) {
+    out[i] = make_uint4(0, 0, 0, 0);
+    if (lse && (i & 7) == 0) lse[i >> 3] = -INFINITY;
+  }
+}
+
+// CTAs that share a row: as many as keep the whole card (two per SM) busy, each with some
+// tiles of the longest possible row.
+constexpr int kSlots = 2 * 148, kTilesPerSplit = 4;
+int splits_of(const Dims &d, int nq) {
+  const long long items = d.BH() * nq;
+  const int tiles = (int)((d.N + 127) / 128);
+  if (items == 0 || items * 2 > kSlots) return 1;
+  return (int)std::max(1ll, std::min((long long)(kSlots / items), (long long)(tiles / kTilesPerSplit)));
+}
+
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+using KernelFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const Params);
+template <int KB>
+KernelFn pick(bool cap, bool bias) {
+  return cap ? (bias ? masked_attn_kernel<KB, true, true> : masked_attn_kernel<KB, true, false>)
+             : (bias ? masked_attn_kernel<KB, false, true> : masked_attn_kernel<KB, false, false>);
+}
+
+}  // namespace
+
+size_t masked_attn_workspace_bytes(const Dims &d, int q_len) {
+  const int nq = (q_len + 127) / 128;
+  const int splits = splits_of(d, nq);
+  size_t n = round256(sizeof(int4) * (size_t)d.B * d.nk);
+  if (splits > 1)
+    n += round256((size_t)d.BH() * nq * splits * 128 * 64 * sizeof(float)) +
+         round256((size_t)d.BH() * nq * splits * 128 * sizeof(float2));
+  return n;
+}
+
+cudaError_t launch_masked_attn(const Dims &d, const MaskedAttnLaunch &a, cudaStream_t st) {
+  const ress_attn_mods &m = a.mods;
+  const int Nq = m.q_len, nq = (Nq + 127) / 128;
+  const long long rows = d.BH() * Nq;
+  if (d.N == 0) {
+    const long long ctas = std::min((rows * 8 + 255) / 256, 4096ll);
+    no_keys_kernel<<<(unsigned)ctas, 256, 0, st>>>(rows, static_cast<uint4 *>(a.out), a.lse);
+    return cudaGetLastError();
+  }
+  CUtensorMap mq, mk, mv;
+  if (!make_map(&mq, a.q, Nq, d.BH(), 128) || !make_map(&mk, a.k, d.N, d.BH(), d.kb) ||
+      !make_map(&mv, a.v, d.N, d.BH(), d.kb))
+    return cudaErrorNotSupported;
+  Params p = {};
+  p.kv_idx = a.kv_idx;
+  p.kv_cnt = a.kv_cnt;
+  p.order = a.order;
+  if (m.slopes) {
+    p.slopes = m.slopes;
+    p.q_pos = m.q_pos;
+    p.k_pos = m.k_pos;
+  }
+  p.q_doc = m.q_doc;
+  p.k_doc = m.k_doc;
+  p.q_order = m.q_order;
+  p.k_order = m.k_order;
+  p.out = static_cast<__nv_bfloat16 *>(a.out);
+  p.lse = a.lse;
+  p.dev_err = a.dev_err;
+  p.H = d.H;
+  p.N = d.N;
+  p.Nq = Nq;
+  p.nq = nq;
+  p.nk = d.nk;
+  p.splits = splits_of(d, nq);
+  p.scale_log2 = a.scale * kLog2e;
+  p.cap_log2 = m.softcap * kLog2e;
+  p.cap_in = m.softcap > 0.f ? a.scale / m.softcap : 0.f;
+  unsigned char *ws = static_cast<unsigned char *>(a.workspace);
+  int4 *blocks = reinterpret_cast<int4 *>(ws);
+  p.blocks = blocks;
+  const long long items = d.BH() * nq;
+  if (p.splits > 1) {
+    ws += round256(sizeof(int4) * (size_t)d.B * d.nk);
+    p.part_o = reinterpret_cast<float *>(ws);
+    ws += round256((size_t)items * p.splits * 128 * 64 * sizeof(float));
+    p.part_ml = reinterpret_cast<float2 *>(ws);
+  }
+  if (m.q_doc || m.q_order) {
+    const long long n = 1ll * d.B * d.nk;
+    summary_kernel<<<(unsigned)((n + 7) / 8), 256, 0, st>>>(m.k_doc, m.k_order, d.N, d.nk, d.kb, n, blocks);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  KernelFn kern = d.kb == 64 ? pick<64>(m.softcap > 0.f, m.slopes != nullptr)
+                             : pick<128>(m.softcap > 0.f, m.slopes != nullptr);
+  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kern),
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3((unsigned)items, (unsigned)p.splits), kThreads, kSmemBytes, st>>>(mq, mk, mv, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.splits == 1) return e;
+  join_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p.part_o, p.part_ml, p.splits, nq, Nq, rows, p.out,
+                                                         p.lse);
+  return cudaGetLastError();
+}
+
+}  // namespace ress

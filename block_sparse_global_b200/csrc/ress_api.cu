@@ -46,6 +46,12 @@ bool ptr_ok(const void *p) { return p != nullptr && aligned16(p); }
 
 ress_status from_cuda(cudaError_t e) { return e == cudaSuccess ? RESS_OK : RESS_ERR_CUDA; }
 
+// Query rows of ress_masked_attn: the grid's limit, and the limits of check_shape for rows.
+bool queries_ok(const Dims &d, int32_t q_len) {
+  const long long nq = (1ll * q_len + ress::kBlock - 1) / ress::kBlock;
+  return nq <= ress::kMaxBlocks && d.BH() * nq <= 0x7fffffffll;
+}
+
 bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
 // ------------------------------------------------------------ checks of the token operators
@@ -564,6 +570,62 @@ ress_status ress_qk_norm_rope(const ress_qk_params *params, const ress_rows *q,
   a.part[1] = {k, k_out, heads[1], true, p.k_weight, p.k_bias};
   a.part[2] = {v, v_out, heads[2], false, nullptr, nullptr};
   return from_cuda(ress::launch_tokens(a, (cudaStream_t)stream));
+}
+
+// ------------------------------------------------------- attention with changed scores
+size_t ress_masked_attn_workspace_bytes(const ress_shape *shape, int32_t q_len) {
+  Dims d;
+  bool empty;
+  if (check_shape(shape, &d, &empty) != RESS_OK || empty || q_len < 1) return 0;
+  if (!queries_ok(d, q_len)) return 0;
+  return ress::masked_attn_workspace_bytes(d, q_len);
+}
+
+ress_status ress_masked_attn(const ress_shape *shape, const ress_attn_mods *mods, const void *q,
+                             const void *k, const void *v, const int32_t *kv_idx,
+                             const int32_t *kv_cnt, const int32_t *work_order, float scale,
+                             void *out, float *lse, void *workspace, size_t workspace_bytes,
+                             int32_t *dev_err, ress_stream_t stream) {
+  Dims d;
+  bool empty;
+  ress_status st = check_shape(shape, &d, &empty);
+  if (st != RESS_OK) return st;
+  ress_attn_mods m = {};
+  m.q_len = d.N;
+  if (mods != nullptr) m = *mods;
+  if (m.q_len < 0 || !(m.softcap >= 0.f) || std::isinf(m.softcap)) return RESS_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || std::isinf(scale)) return RESS_ERR_INVALID_ARG;
+  if ((m.q_pos == nullptr) != (m.k_pos == nullptr) || (m.q_doc == nullptr) != (m.k_doc == nullptr) ||
+      (m.q_order == nullptr) != (m.k_order == nullptr))
+    return RESS_ERR_INVALID_ARG;
+  if (m.slopes != nullptr && m.q_pos == nullptr) return RESS_ERR_INVALID_ARG;
+  for (const void *x : {(const void *)m.slopes, (const void *)m.q_pos, (const void *)m.k_pos, (const void *)m.q_doc,
+                        (const void *)m.k_doc, (const void *)m.q_order, (const void *)m.k_order, (const void *)lse,
+                        (const void *)dev_err})
+    if (!aligned_to(x, 4)) return RESS_ERR_INVALID_ARG;
+  if ((kv_idx == nullptr) != (kv_cnt == nullptr)) return RESS_ERR_INVALID_ARG;
+  if (!queries_ok(d, m.q_len)) return RESS_ERR_UNSUPPORTED;
+  if (d.B == 0 || m.q_len == 0) return RESS_OK;
+  if (!ptr_ok(out)) return RESS_ERR_INVALID_ARG;
+  if (d.N > 0) {
+    if (!ptr_ok(q) || !ptr_ok(k) || !ptr_ok(v) || !ptr_ok(workspace)) return RESS_ERR_INVALID_ARG;
+    if (!aligned16(kv_idx) || !aligned16(kv_cnt) || !aligned16(work_order)) return RESS_ERR_INVALID_ARG;
+    if (workspace_bytes < ress::masked_attn_workspace_bytes(d, m.q_len)) return RESS_ERR_INVALID_ARG;
+  }
+  ress::MaskedAttnLaunch a;
+  a.mods = m;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.kv_idx = kv_idx;
+  a.kv_cnt = kv_cnt;
+  a.order = work_order;
+  a.scale = scale;
+  a.out = out;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.dev_err = dev_err;
+  return from_cuda(ress::launch_masked_attn(d, a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

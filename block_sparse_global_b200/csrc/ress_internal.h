@@ -110,4 +110,18 @@ struct TokensLaunch {
 };
 cudaError_t launch_tokens(const TokensLaunch &a, cudaStream_t st);
 
+// Attention over kept blocks with changed scores; d.nk key blocks, mods.q_len queries.
+struct MaskedAttnLaunch {
+  ress_attn_mods mods;
+  const void *q, *k, *v;
+  const int32_t *kv_idx, *kv_cnt, *order;
+  float scale;
+  void *out;
+  float *lse;
+  void *workspace;
+  int32_t *dev_err;
+};
+size_t masked_attn_workspace_bytes(const Dims &d, int q_len);
+cudaError_t launch_masked_attn(const Dims &d, const MaskedAttnLaunch &a, cudaStream_t st);
+
 }  // namespace ress

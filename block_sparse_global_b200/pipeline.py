@@ -135,13 +135,42 @@ class SparseGlobalAttention:
                                  self.order if schedule else None, self.scale, self.out, self.lse,
                                  self.dev_err, stream)
 
+    def attend_masked(self, q, k, v, kept: bool = True, out=None, lse=None, schedule: bool = True,
+                      stream=None, **mods):
+        """Attention with changed scores (`mods`: softcap, slopes, q_/k_ pos, doc and order, as
+        for ress_masked_attn) of q [B,H,q_len,64] over this layer's k, v.  kept: over the
+        selected blocks, for all of the sequence's tokens (q_len = N); otherwise over every
+        block, for any q_len (new tokens over a cache).  Without `out`, the result goes to
+        the layer's out and lse if q_len = N, else to a new tensor."""
+        n = q.shape[2]
+        if kept and n != self.N:
+            raise ValueError("the kept blocks are those of the sequence's own tokens")
+        if out is None:
+            if n == self.N:
+                out, lse = self.out, self.lse if lse is None else lse
+            else:
+                out = torch.empty(self.B, self.H, n, 64, device=self.device, dtype=torch.bfloat16)
+        need = R.ress_masked_attn_workspace_bytes(self.shape, n)
+        ws = getattr(self, "_masked_ws", None)
+        if ws is None or ws.numel() < need:
+            ws = self._masked_ws = torch.empty(need, device=self.device, dtype=torch.uint8)
+        if kept and schedule:
+            R.ress_attn_schedule(self.shape, self.kv_cnt, self.order, stream)
+        R.ress_masked_attn(self.shape, q, k, v, self.kv_idx if kept else None,
+                           self.kv_cnt if kept else None, self.order if kept and schedule else None,
+                           self.scale, out, lse, workspace=ws, dev_err=self.dev_err[:1],
+                           stream=stream, **mods)
+        return out
+
     def forward(self, q, k, v, method: int, budgets: Sequence[int], keep_k=None, dense_q=None,
                 rounds: int = 0, rho: float = 0.5, eps: float = 1e-4, seed: int = 0, stream=None,
-                top_p: float = 1.0, write_scores: bool = False, fused: bool = True):
+                top_p: float = 1.0, write_scores: bool = False, fused: bool = True,
+                mods: Optional[dict] = None):
         """pool -> block map + selection (one kernel: drift_select for DRIFT, scores_select
         otherwise; with fused=False, DRIFT runs the separate block-map, drift and selection
         calls) -> schedule -> attention.  write_scores: the fused kernels also write P,
-        v_bar (and s for DRIFT)."""
+        v_bar (and s for DRIFT).  mods: the attention is attend_masked() with these changes of
+        the scores (the selection does not see them)."""
         self.pool(q, k, v, stream)
         if method == R.SELECT_DRIFT and fused:
             self.drift_select(budgets, keep_k, dense_q, rounds, rho, eps, stream,
@@ -154,7 +183,10 @@ class SparseGlobalAttention:
         else:
             self.scores_select(method, budgets, keep_k, dense_q, seed, write_scores, stream=stream,
                                top_p=top_p)
-        self.attend(q, k, v, stream)
+        if mods is None:
+            self.attend(q, k, v, stream)
+        else:
+            self.attend_masked(q, k, v, stream=stream, **mods)
         return self.out
 
     # ------------------------------------------------------------- CUDA graphs

@@ -72,6 +72,12 @@ class ress_qk_params(ctypes.Structure):
                 ("specials", ctypes.c_int32)]
 
 
+class ress_attn_mods(ctypes.Structure):
+    _fields_ = [("q_len", ctypes.c_int32), ("softcap", ctypes.c_float)] + [
+        (n, ctypes.c_void_p) for n in ("slopes", "q_pos", "k_pos", "q_doc", "k_doc", "q_order",
+                                       "k_order")]
+
+
 _lib = None
 _lock = threading.Lock()
 _VP, _I32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
@@ -102,6 +108,10 @@ _SIGS = {
     "ress_debug_attn_forced_timeout": (_I32, [ctypes.POINTER(ress_shape), _VP, _VP, _VP, _VP,
                                               _VP, ctypes.c_float, _VP, _VP, ctypes.c_int64,
                                               _VP]),
+    "ress_masked_attn_workspace_bytes": (_SZ, [ctypes.POINTER(ress_shape), _I32]),
+    "ress_masked_attn": (_I32, [ctypes.POINTER(ress_shape), ctypes.POINTER(ress_attn_mods), _VP,
+                                _VP, _VP, _VP, _VP, _VP, ctypes.c_float, _VP, _VP, _VP, _SZ, _VP,
+                                _VP]),
     "ress_rope_init": (_I32, [ctypes.POINTER(ress_rope_plan), _I32, _I32, _I32, _I32,
                               ctypes.c_double, _I32, ctypes.c_double, _I32, ctypes.c_double,
                               ctypes.c_double]),
@@ -416,3 +426,54 @@ def ress_qk_norm_rope(q, k, q_out, k_out, v=None, v_out=None, norm: int = NORM_R
                        int(specials))
     _launch("ress_qk_norm_rope", q.device, stream, ctypes.byref(p),
             *[None if r is None else ctypes.byref(r) for r in rows])
+
+
+# ------------------------------------------------------- attention with changed scores
+def ress_masked_attn_workspace_bytes(shape, q_len: int) -> int:
+    return int(load().ress_masked_attn_workspace_bytes(ctypes.byref(_shape(shape)), int(q_len)))
+
+
+def _sized(t: Optional[torch.Tensor], shape, dtype, device, name: str):
+    """Device pointer of a contiguous tensor of exactly this shape, type and device, or None."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return _ptr(t)
+
+
+def ress_masked_attn(shape, q, k, v, kv_idx, kv_cnt, work_order, scale: float, out, lse=None,
+                     softcap: float = 0.0, slopes=None, q_pos=None, k_pos=None, q_doc=None,
+                     k_doc=None, q_order=None, k_order=None, workspace=None, dev_err=None,
+                     stream=None):
+    """Attention over kept blocks with capped scores, a distance bias and document and order
+    masks, for all tokens or for others: q [B,H,q_len,64] over k, v [B,H,N,64].  kv_idx and
+    kv_cnt None: every key block.  `workspace`: uint8, ress_masked_attn_workspace_bytes."""
+    s = _shape(shape)
+    dev = q.device
+    if q.dim() != 4:
+        raise ValueError("expected q [B, H, q_len, 64]")
+    B, H, N, n = s.batch, s.heads, s.seq_len, q.shape[2]
+    nq, nk = grid(n)[0], grid(N, s.key_block)[1]
+    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    qd, kd = (B, n), (B, N)
+    m = ress_attn_mods(n, float(softcap), _sized(slopes, (H,), f32, dev, "slopes"),
+                       _sized(q_pos, qd, i32, dev, "q_pos"), _sized(k_pos, kd, i32, dev, "k_pos"),
+                       _sized(q_doc, qd, i32, dev, "q_doc"), _sized(k_doc, kd, i32, dev, "k_doc"),
+                       _sized(q_order, qd, i32, dev, "q_order"),
+                       _sized(k_order, kd, i32, dev, "k_order"))
+    nbytes = 0
+    if workspace is not None:
+        if workspace.device != dev:
+            raise ValueError("the workspace is on another device")
+        nbytes = workspace.numel() * workspace.element_size()
+    if work_order is not None and work_order.numel() != B * H * nq:
+        raise ValueError("work_order holds one entry per row")
+    _launch("ress_masked_attn", dev, stream, ctypes.byref(s), ctypes.byref(m),
+            _sized(q, (B, H, n, 64), bf, dev, "q"), _sized(k, (B, H, N, 64), bf, dev, "k"),
+            _sized(v, (B, H, N, 64), bf, dev, "v"),
+            _sized(kv_idx, (B, H, nq, nk), i32, dev, "kv_idx"),
+            _sized(kv_cnt, (B, H, nq), i32, dev, "kv_cnt"), _ptr(work_order), float(scale),
+            _sized(out, (B, H, n, 64), bf, dev, "out"), _sized(lse, (B, H, n), f32, dev, "lse"),
+            _ptr(workspace), nbytes, _ptr(dev_err))

@@ -16,7 +16,8 @@
  * per layer at model load) and a longest-first launch order for (5)
  * (ress_attn_schedule).  Around them stand the operators that a layer's queries and keys
  * go through first, the per-head norm and the rotary positions (ress_qk_norm_rope,
- * ress_rope).
+ * ress_rope), and attention over the kept blocks with capped scores, a distance bias, and
+ * document and order masks (ress_masked_attn).
  *
  * Sources, cited by page title and section / equation:
  *   [ReSS]       "ReSS: Residual-Restoring Sparse Attention for 3D Vision Transformers"
@@ -141,8 +142,8 @@ typedef struct {
 /* Version of this ABI (incremented on any change that an earlier caller could meet): 5
  * (version 4: ress_shape gained `key_block`; ress_select_params gained `objective`, `top_p`
  * and `drift`; RESS_SELECT_CDF; version 5: ress_drift_select and its workspace query).  The
- * token operators (ress_rope, ress_qk_norm_rope) were added to version 5; they change no
- * call or struct that was there. */
+ * token operators (ress_rope, ress_qk_norm_rope) and ress_masked_attn were added to version
+ * 5; they change no call or struct that was there. */
 int32_t ress_abi_version(void);
 
 /* Human-readable name of a status code (static string). */
@@ -515,6 +516,63 @@ ress_status ress_qk_norm_rope(const ress_qk_params *params, const ress_rows *q,
                               const ress_rows *k, const ress_rows *v, const ress_rows *q_out,
                               const ress_rows *k_out, const ress_rows *v_out,
                               ress_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Attention over kept blocks with changed scores.
+ * ---------------------------------------------------------------------------------- */
+
+/* What ress_masked_attn does to the scores.  Every array may be NULL; a query array and its
+ * key array are given together.  k_* are DEVICE int32 [B, N], q_* DEVICE int32 [B, Nq]; the
+ * same array may serve as both where Nq = N.  These arrays and `slopes` need 4-byte
+ * alignment only, so that q_* may be the end of k_*. */
+typedef struct {
+  int32_t q_len;                  /* Nq >= 0: query tokens of each batch element            */
+  float softcap;                  /* c >= 0, finite: scores become c tanh(score / c); 0: as
+                                     they are                                                */
+  const float *slopes;            /* DEVICE fp32 [H], finite: slopes[h] * |q_pos - k_pos| is
+                                     taken off the (capped) scores; needs q_pos and k_pos    */
+  const int32_t *q_pos, *k_pos;   /* positions, |pos| <= 2^24 (beyond, distances round)      */
+  const int32_t *q_doc, *k_doc;   /* documents: a query sees the keys of its own document.  A
+                                     negative document is padding: it sees and is seen by none */
+  const int32_t *q_order, *k_order; /* a query sees keys with k_order <= q_order: the token's
+                                     index for causal attention, its view's index for
+                                     attention that is causal over views, and
+                                     max(0, index - prefix + 1) for a prefix seen by all     */
+} ress_attn_mods;
+
+/* Bytes of device workspace that ress_masked_attn needs for `shape` with q_len query tokens. */
+size_t ress_masked_attn_workspace_bytes(const ress_shape *shape, int32_t q_len);
+
+/*
+ * ress_masked_attn -- ress_block_sparse_attn with changed scores, for the sequence's own
+ * tokens or for others (new tokens over a cache: q_len of them).  For every query token t of
+ * head (b,h) and every key u that t sees (in a kept block, of t's document, not later in
+ * order)
+ *   z(t,u) = cap(scale * q_t . k_u) - slopes[h] * |q_pos[t] - k_pos[u]|
+ *   out[b,h,t,:] = sum_u softmax_u(z(t,u)) v_u,     lse[b,h,t] = ln sum_u exp z(t,u).
+ * A query that sees no key gets a zero row and lse = -inf (so does one whose scores are all
+ * -inf, or below -2e38).  A key that a mask hides from a query does not reach its row,
+ * whatever it holds (infinities and NaN included).  fp32 scores, maximum and sums; the
+ * weights are rounded to bf16 before they meet the values, and the output once at the end.
+ *   shape    N = seq_len keys; query blocks are of 128 tokens, nq = ceil(q_len / 128).
+ *   q [B,H,q_len,64]; k, v [B,H,N,64]; out [B,H,q_len,64], all bf16; lse fp32 [B,H,q_len]
+ *            or NULL.
+ *   kv_idx   int32 [B,H,nq,nk] and kv_cnt int32 [B,H,nq], as for ress_block_sparse_attn; or
+ *            both NULL: every key block is kept.  Blocks that no query of a row sees are
+ *            passed over unread.  A block listed twice counts twice.
+ *   work_order int32 [B*H*nq] permutation or NULL.  Outputs do not depend on it.
+ *   mods     HOST; NULL: q_len = N and scores as they are.
+ *   workspace  DEVICE scratch of at least ress_masked_attn_workspace_bytes(shape, q_len)
+ *            bytes, 16-byte aligned, overwritten; calls that may overlap in time need one
+ *            each.
+ *   dev_err  as for ress_block_sparse_attn (a row with a bad list is left unwritten).
+ * N = 0 with q_len > 0 writes zero rows and lse = -inf (no workspace needed).
+ */
+ress_status ress_masked_attn(const ress_shape *shape, const ress_attn_mods *mods, const void *q,
+                             const void *k, const void *v, const int32_t *kv_idx,
+                             const int32_t *kv_cnt, const int32_t *work_order, float scale,
+                             void *out, float *lse, void *workspace, size_t workspace_bytes,
+                             int32_t *dev_err, ress_stream_t stream);
 
 #ifdef __cplusplus
 }
