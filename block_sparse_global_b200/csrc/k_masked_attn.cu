@@ -93,21 +93,52 @@ RESS_DEV bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
 }
 RESS_DEV void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// tanh(y) = 1 - 2 / (1 + e^2y) has an absolute error of an fp32 unit; below 1/2 the odd
-// series keeps the relative one (terms to y^13; the next is below 1e-7 of the sum at 1/2).
-RESS_DEV float tanh_small(float y) {
-  const float y2 = y * y;
-  float t = 21844.0f / 6081075.0f;
-  t = fmaf(t, y2, -1382.0f / 155925.0f);
-  t = fmaf(t, y2, 62.0f / 2835.0f);
-  t = fmaf(t, y2, -17.0f / 315.0f);
-  t = fmaf(t, y2, 2.0f / 15.0f);
-  t = fmaf(t, y2, -1.0f / 3.0f);
-  return fmaf(t * y2, y, y);
+RESS_DEV uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
-RESS_DEV float tanh_full(float y) {
-  const float r = rcp_approx(1.0f + ex2_approx(2.0f * kLog2e * y));
-  return fabsf(y) < 0.5f ? tanh_small(y) : fmaf(-2.0f, r, 1.0f);
+
+// tanh(y) / y as a polynomial in y^2, fitted here for minimax relative error (Lawson's
+// iteratively reweighted least squares): up to |y| = 1/2 (1.3e-8; 1.1e-7 evaluated in fp32)
+// and up to |y| = 1 (5e-8; 1.6e-7).
+template <int N>
+RESS_DEV constexpr float tanh_fit(int k) {
+  constexpr float c4[5] = {1.000000000e+00f, -3.333306909e-01f, 1.332477927e-01f, -5.298607424e-02f,
+                           1.713500544e-02f};
+  constexpr float c6[7] = {9.999999404e-01f, -3.333283961e-01f, 1.332520396e-01f, -5.345702916e-02f,
+                           2.028998174e-02f, -6.203379016e-03f, 1.041022479e-03f};
+  return N == 4 ? c4[k < 5 ? k : 4] : c6[k];
+}
+
+// s <- tanh(s in) of a row's 128 scores, by the polynomial.
+template <int N>
+RESS_DEV void cap_small(uint32_t (&sv)[128], float in) {
+  const uint64_t in2 = f2(in, in);
+#pragma unroll
+  for (int c = 0; c < 128; c += 2) {
+    const uint64_t y = fmul2(f2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), in2);
+    const uint64_t t = fmul2(y, y);
+    uint64_t a = f2(tanh_fit<N>(N), tanh_fit<N>(N));
+#pragma unroll
+    for (int k = N - 1; k >= 0; --k) a = ffma2(a, t, f2(tanh_fit<N>(k), tanh_fit<N>(k)));
+    const uint64_t u = fmul2(a, y);
+    sv[c] = __float_as_uint(f2lo(u));
+    sv[c + 1] = __float_as_uint(f2hi(u));
+  }
+}
+// Any score: 1 - 2 / (1 + e^2y) is off by an fp32 unit absolutely, the polynomial below
+// |y| = 1/2 relatively.
+RESS_DEV void cap_any(uint32_t (&sv)[128], float in) {
+#pragma unroll
+  for (int c = 0; c < 128; ++c) {
+    const float y = __uint_as_float(sv[c]) * in, t = y * y;
+    float a = tanh_fit<4>(4);
+#pragma unroll
+    for (int k = 3; k >= 0; --k) a = fmaf(a, t, tanh_fit<4>(k));
+    const float r = rcp_approx(1.0f + ex2_approx(2.0f * kLog2e * y));
+    sv[c] = __float_as_uint(fabsf(y) < 0.5f ? a * y : fmaf(-2.0f, r, 1.0f));
+  }
 }
 
 struct Params {
@@ -124,6 +155,7 @@ struct Params {
   int splits;
   float scale_log2;         // without a cap
   float cap_log2, cap_in;   // c log2 e; scale / c
+  float cap_half;           // scores up to this stay within |y| = 1/2
 };
 
 // KB tokens per key block; CAP, BIAS: the score changes compiled in.
@@ -373,9 +405,17 @@ __global__ void __launch_bounds__(kThreads, 2)
       int *m_doc = reinterpret_cast<int *>(smem + kOffMeta) + warp * 3 * 128;
       int *m_order = m_doc + 128;
       float *m_pos = reinterpret_cast<float *>(m_doc + 256);
+      // positions relative to the row block's first query: exact small numbers
+      long long ref = 0;
+      int q_lo = 0, q_hi = 0;  // positions of the warp's queries
       float row_pos = 0.f, slope = 0.f;
       if constexpr (BIAS) {
-        row_pos = t < p.Nq ? (float)p.q_pos[(long long)b * p.Nq + t] : 0.f;
+        const int32_t *qp = p.q_pos + (long long)b * p.Nq;
+        ref = qp[qi * 128];
+        const int mine_pos = qp[min(t, p.Nq - 1)];
+        q_lo = __reduce_min_sync(0xffffffffu, mine_pos);
+        q_hi = __reduce_max_sync(0xffffffffu, mine_pos);
+        row_pos = (float)(mine_pos - ref);
         slope = -p.slopes[h] * kLog2e;
       }
       float m_run = kNoMax, l_run = 0.f;
@@ -396,18 +436,39 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           return u < p.N ? u : -1;
         };
+        // +1: every key lies at or before every query of the warp, -1: at or after, 0: mixed
+        int side = 0;
+        bool gaps = false;  // columns without a key
         if (BIAS || partial) {
           __syncwarp();  // the last tile's values have been read
+          int pos[4], lo = INT_MAX, hi = INT_MIN;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int c = lane + 32 * i, u = key_of(c);
             const long long at = (long long)b * p.N + u;
-            if constexpr (BIAS) m_pos[c] = u >= 0 ? (float)__ldg(p.k_pos + at) : 0.f;
+            if constexpr (BIAS) {
+              pos[i] = u >= 0 ? __ldg(p.k_pos + at) : (int)ref;
+              if (u >= 0) {
+                lo = min(lo, pos[i]);
+                hi = max(hi, pos[i]);
+              }
+            }
+            gaps |= u < 0;
             if (partial) {
               m_doc[c] = u < 0 ? -1 : (p.k_doc ? max(__ldg(p.k_doc + at), -1) : 0);
               m_order[c] = u < 0 || !p.k_order ? 0 : __ldg(p.k_order + at);
             }
           }
+          if constexpr (BIAS) {
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            hi = __reduce_max_sync(0xffffffffu, hi);
+            side = hi <= q_lo ? 1 : (lo >= q_hi ? -1 : 0);
+            // on one side the bias is a term of the row plus one of the column
+            const float f = side == 0 ? 1.0f : (side > 0 ? -slope : slope);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m_pos[lane + 32 * i] = (float)(pos[i] - ref) * f;
+          }
+          gaps = __any_sync(0xffffffffu, gaps);
           __syncwarp();
         }
         ok = warp_wait(&bar->s_full, j & 1, abort);
@@ -421,33 +482,72 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->s_free);
+        // z = sv * sc + shift from here on
+        float sc = p.scale_log2, shift = 0.f;
         if constexpr (CAP) {
+          float mc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            sv[c] = __float_as_uint(p.cap_log2 * tanh_full(__uint_as_float(sv[c]) * p.cap_in));
+          for (int c = 0; c < 128; c += 8) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              mc[q] = fmax3(mc[q], fabsf(__uint_as_float(sv[c + 2 * q])), fabsf(__uint_as_float(sv[c + 2 * q + 1])));
+          }
+          const float big = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
+          if (__all_sync(0xffffffffu, big <= p.cap_half))
+            cap_small<4>(sv, p.cap_in);
+          else if (__all_sync(0xffffffffu, big <= 2.0f * p.cap_half))
+            cap_small<6>(sv, p.cap_in);
+          else
+            cap_any(sv, p.cap_in);
+          sc = p.cap_log2;
         }
         if constexpr (BIAS) {
+          if (side != 0) {
+            shift = (side > 0 ? slope : -slope) * row_pos;
+            const uint64_t sc2 = f2(sc, sc);
 #pragma unroll
-          for (int c = 0; c < 128; c += 4) {
-            const float4 kp = *reinterpret_cast<const float4 *>(m_pos + c);
-            const float d[4] = {fabsf(row_pos - kp.x), fabsf(row_pos - kp.y), fabsf(row_pos - kp.z),
-                                fabsf(row_pos - kp.w)};
+            for (int c = 0; c < 128; c += 4) {
+              const ulonglong2 kp = *reinterpret_cast<const ulonglong2 *>(m_pos + c);
+              const uint64_t z0 = ffma2(f2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sc2, kp.x);
+              const uint64_t z1 = ffma2(f2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), sc2, kp.y);
+              sv[c] = (uint32_t)z0;
+              sv[c + 1] = (uint32_t)(z0 >> 32);
+              sv[c + 2] = (uint32_t)z1;
+              sv[c + 3] = (uint32_t)(z1 >> 32);
+            }
+          } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float z = CAP ? __uint_as_float(sv[c + i]) : __uint_as_float(sv[c + i]) * p.scale_log2;
-              sv[c + i] = __float_as_uint(fmaf(slope, d[i], z));
+            for (int c = 0; c < 128; c += 4) {
+              const float4 kp = *reinterpret_cast<const float4 *>(m_pos + c);
+              const float d[4] = {fabsf(row_pos - kp.x), fabsf(row_pos - kp.y), fabsf(row_pos - kp.z),
+                                  fabsf(row_pos - kp.w)};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                sv[c + i] = __float_as_uint(fmaf(slope, d[i], __uint_as_float(sv[c + i]) * sc));
             }
           }
+          sc = 1.0f;
         }
         if (partial) {
+          if (p.q_doc || gaps) {
 #pragma unroll
-          for (int c = 0; c < 128; c += 4) {
-            const int4 kd = *reinterpret_cast<const int4 *>(m_doc + c);
-            const int4 ko = *reinterpret_cast<const int4 *>(m_order + c);
-            if (kd.x != row_doc || ko.x > row_order) sv[c] = __float_as_uint(-INFINITY);
-            if (kd.y != row_doc || ko.y > row_order) sv[c + 1] = __float_as_uint(-INFINITY);
-            if (kd.z != row_doc || ko.z > row_order) sv[c + 2] = __float_as_uint(-INFINITY);
-            if (kd.w != row_doc || ko.w > row_order) sv[c + 3] = __float_as_uint(-INFINITY);
+            for (int c = 0; c < 128; c += 4) {
+              const int4 kd = *reinterpret_cast<const int4 *>(m_doc + c);
+              if (kd.x != row_doc) sv[c] = __float_as_uint(-INFINITY);
+              if (kd.y != row_doc) sv[c + 1] = __float_as_uint(-INFINITY);
+              if (kd.z != row_doc) sv[c + 2] = __float_as_uint(-INFINITY);
+              if (kd.w != row_doc) sv[c + 3] = __float_as_uint(-INFINITY);
+            }
+          }
+          if (p.q_order) {
+#pragma unroll
+            for (int c = 0; c < 128; c += 4) {
+              const int4 ko = *reinterpret_cast<const int4 *>(m_order + c);
+              if (ko.x > row_order) sv[c] = __float_as_uint(-INFINITY);
+              if (ko.y > row_order) sv[c + 1] = __float_as_uint(-INFINITY);
+              if (ko.z > row_order) sv[c + 2] = __float_as_uint(-INFINITY);
+              if (ko.w > row_order) sv[c + 3] = __float_as_uint(-INFINITY);
+            }
           }
         }
         // values of a partial tile that are not finite: which rows of V hold one
@@ -488,20 +588,19 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int q = 0; q < 4; ++q)
             mc[q] = fmax3(mc[q], __uint_as_float(sv[c + 2 * q]), __uint_as_float(sv[c + 2 * q + 1]));
         }
-        const float sc = CAP || BIAS ? 1.0f : p.scale_log2;
         const float mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
-        const float m_new = fmaxf(m_run, mx * sc);
+        const float m_new = fmaxf(m_run, fmaf(mx, sc, shift));
         const bool rescale = m_new > m_run + kRescaleLog2;
         const float m_use = rescale ? m_new : m_run;
         const float alpha = rescale ? ex2_approx(m_run - m_new) : 1.0f;
         const uint64_t sc2 = f2(sc, sc);
-        const uint64_t nm2 = f2(-m_use, -m_use);
+        const uint64_t nm2 = f2(shift - m_use, shift - m_use);
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
         uint32_t pk[64];
 #pragma unroll
         for (int c = 0; c < 64; ++c) {
           const uint64_t s2 = f2(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1]));
-          const uint64_t z = CAP || BIAS ? fadd2(s2, nm2) : ffma2(s2, sc2, nm2);
+          const uint64_t z = BIAS ? fadd2(s2, nm2) : ffma2(s2, sc2, nm2);
           const uint64_t e = f2(ex2_approx(f2lo(z)), ex2_approx(f2hi(z)));
           acc[c & 3] = fadd2(acc[c & 3], e);
           pk[c] = pack_bf16x2(f2lo(e), f2hi(e));
@@ -774,6 +873,7 @@ cudaError_t launch_masked_attn(const Dims &d, const MaskedAttnLaunch &a, cudaStr
   p.scale_log2 = a.scale * kLog2e;
   p.cap_log2 = m.softcap * kLog2e;
   p.cap_in = m.softcap > 0.f ? a.scale / m.softcap : 0.f;
+  p.cap_half = 0.5f / p.cap_in;
   unsigned char *ws = static_cast<unsigned char *>(a.workspace);
   int4 *blocks = reinterpret_cast<int4 *>(ws);
   p.blocks = blocks;
