@@ -13,20 +13,23 @@
 // Work split.  One CTA per (batch, head, query block of 128) row; two CTAs share an SM.  A
 // CTA first walks its list of kept blocks against the blocks' summaries (smallest and
 // largest document and order, one int4 per key block, written by summary_kernel) and keeps
-// in shared memory the blocks that some query of the row sees, each marked whole (every
-// pair visible) or partial.  Blocks that nobody sees cost no load and no product; whole
-// blocks take no per-element test.  When the rows are few, `splits` CTAs share a row: each
-// takes a contiguous part of its tiles and writes its unnormalised sums, and join_kernel
-// weighs them together.
+// in shared memory the blocks that some query of the row sees, with a class for each softmax
+// warp: whole (its 32 queries see every key), none, or mixed.  Blocks that nobody sees cost
+// no load and no product; only mixed tiles test element by element, and a warp that sees
+// nothing of a tile stores zero weights.  When the rows are few, `splits` CTAs share a row:
+// each takes a contiguous part of its tiles and writes its unnormalised sums, and
+// join_kernel weighs them together.
 //
 // Warp roles are those of k_attn.cu (192 threads): warps 0-3 softmax, one query row per
 // thread; warp 4 the TMA producer; warp 5 the tensor-core issuer.  Tensor memory: S columns
 // [0,128), P [128,192), O [192,256).
 //
 // Masked values.  P of a masked pair is exactly 0, but 0 times an infinite or NaN value is
-// NaN inside the matrix product.  In partial tiles of a masked call the softmax warps
-// therefore look at the tile's values: if one is not finite, it is added by hand to the
-// rows that see its token, and replaced by 0 in shared memory before the product.
+// NaN inside the matrix product.  A masked call therefore looks at its finished rows: if one
+// that saw a key is not finite, the CTA walks its tiles a second time, and there the softmax
+// warps look at the values of every tile that is not whole for all of them; those that are
+// not finite are added by hand to the rows that see their token, and replaced by 0 in shared
+// memory before the product.  Finite inputs pay 64 tests per row for this.
 #include <algorithm>
 #include <climits>
 
@@ -48,14 +51,17 @@ constexpr int kTile = 128 * 64 * 2;  // bytes of one 128 x 64 bf16 tile
 constexpr int kOffQ = 0;
 constexpr int kOffK = kTile;
 constexpr int kOffV = kOffK + kKStages * kTile;
-constexpr int kOffList = kOffV + kVStages * kTile;         // uint16 per kept block
-constexpr int kOffMeta = kOffList + 2 * kMaxBlocks;        // per softmax warp: doc, order, pos
-constexpr int kOffBar = kOffMeta + 4 * 3 * 128 * 4;
+constexpr int kOffList = kOffV + kVStages * kTile;   // uint16 per kept block: its index
+constexpr int kOffClass = kOffList + 2 * kMaxBlocks;  // uint8: two bits per softmax warp
+constexpr int kOffMeta = kOffClass + kMaxBlocks;      // a mixed tile's documents and orders
+constexpr int kOffPos = kOffMeta + 2 * 128 * 4;       // per softmax warp: the tile's positions
+constexpr int kOffBar = kOffPos + 4 * 128 * 4;
 constexpr int kSmemBytes = kOffBar + 384 + 1024;
 static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
 constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 192;
-constexpr uint16_t kPartial = 0x8000;  // list entry: block index, and this if not whole
+constexpr int kUneven = INT_MIN;  // step of a block whose positions do not run evenly
+constexpr uint32_t kWhole = 0, kMixed = 1, kNone = 2;  // what a warp sees of a block
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -71,13 +77,15 @@ struct Bars {
   uint64_t o_done;
   uint64_t o_half;
   uint64_t drain;
-  uint64_t scan;  // the softmax warps' look at a partial tile's values
+  uint64_t meet;  // the softmax warps meet: around a mixed tile's arrays and a tile's values
   uint32_t tmem_base;
+  // the row, for the softmax loop: kept here because its registers are full
+  int b, bh, qi, active, skip, tiles, entries;
   int abort;
   int o_init;           // O was started by hand: the first product adds to it
   int count[kWarps];    // filter: visible blocks of each warp's entries
   int qsum[4][5];       // filter: each softmax warp's query summary
-  uint32_t vflag[2][4];  // rows of V (32 per word) that hold a value that is not finite
+  uint32_t vflag[4];    // rows of V (32 per word) that hold a value that is not finite
 };
 static_assert(sizeof(Bars) <= 384, "barriers fit their shared-memory slot");
 
@@ -100,8 +108,9 @@ RESS_DEV uint64_t fmul2(uint64_t a, uint64_t b) {
 }
 
 // tanh(y) / y as a polynomial in y^2, fitted here for minimax relative error (Lawson's
-// iteratively reweighted least squares): up to |y| = 1/2 (1.3e-8; 1.1e-7 evaluated in fp32)
-// and up to |y| = 1 (5e-8; 1.6e-7).
+// iteratively reweighted least squares): up to |y| = 3/8 (degree 3, 5.9e-8), up to 1/2
+// (degree 4, 1.3e-8; 1.1e-7 evaluated in fp32) and up to 1 (degree 6, 5e-8; 1.6e-7).
+constexpr double kTanhFit3[4] = {9.999999404e-01, -3.333197534e-01, 1.328450292e-01, -4.827226326e-02};
 template <int N>
 RESS_DEV constexpr float tanh_fit(int k) {
   constexpr float c4[5] = {1.000000000e+00f, -3.333306909e-01f, 1.332477927e-01f, -5.298607424e-02f,
@@ -145,17 +154,20 @@ struct Params {
   const int32_t *kv_idx, *kv_cnt, *order;
   const int32_t *q_pos, *k_pos, *q_doc, *k_doc, *q_order, *k_order;
   const float *slopes;
-  const int4 *blocks;  // [B][nk]: smallest and largest document, smallest and largest order
+  // [2][B][nk]: smallest and largest document, smallest and largest order of each key block;
+  // and its smallest, largest and first position with the step from token to token
+  const int4 *blocks;
   __nv_bfloat16 *out;
   float *lse;
   float *part_o;    // [items][splits][128][64]
   float2 *part_ml;  // [items][splits][128]
   int32_t *dev_err;
-  int H, N, Nq, nq, nk;
+  int B, H, N, Nq, nq, nk;
   int splits;
   float scale_log2;         // without a cap
   float cap_log2, cap_in;   // c log2 e; scale / c
   float cap_half;           // scores up to this stay within |y| = 1/2
+  float cap_a, cap_k[4];    // and up to this (|y| = 3/8) the cap is s cap_k(s^2), log2 domain
 };
 
 // KB tokens per key block; CAP, BIAS: the score changes compiled in.
@@ -168,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Bars *bar = reinterpret_cast<Bars *>(smem + kOffBar);
   uint16_t *list = reinterpret_cast<uint16_t *>(smem + kOffList);
+  uint8_t *classes = smem + kOffClass;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   // rows of a head from its last query block to its first: under an order mask the long
@@ -176,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const long long item = p.order ? (long long)p.order[x] : x / p.nq * p.nq + (p.nq - 1 - (int)(x % p.nq));
   const long long bh = item / p.nq;
   const int qi = (int)(item - bh * p.nq);
-  const int b = (int)(bh / p.H), h = (int)(bh - (long long)b * p.H);
+  const int b = (int)(bh / p.H);
   const bool masked = p.q_doc != nullptr || p.q_order != nullptr;
 
   // softmax warps that hold a query (the others stay out: their rows of S, P and O are
@@ -199,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     mbar_init(&bar->o_done, 1);
     mbar_init(&bar->o_half, 1);
     mbar_init(&bar->drain, 1);
-    mbar_init(&bar->scan, active);
+    mbar_init(&bar->meet, active);
     bar->abort = 0;
     bar->o_init = 0;
     fence_mbar_init();
@@ -211,8 +224,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   // ---------------------------------------------------------------- the row's blocks
   const int t = qi * 128 + tid;  // query token of a softmax thread
-  int row_doc = 0, row_order = 0;
   if (warp < 4) {
+    int row_doc = 0, row_order = 0;
     const bool there = t < p.Nq;
     if (p.q_doc) row_doc = there ? p.q_doc[(long long)b * p.Nq + t] : -1;
     if (p.q_order) row_order = there ? p.q_order[(long long)b * p.Nq + t] : 0;
@@ -227,17 +240,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     v[4] = __reduce_or_sync(0xffffffffu, v[4]);
     if (lane == 0)
       for (int i = 0; i < 5; ++i) bar->qsum[warp][i] = v[i];
-    if (row_doc < 0) row_doc = -2;  // equal to no key's document
   }
   __syncthreads();
-  int q_dmin = INT_MAX, q_dmax = INT_MIN, q_omin = INT_MAX, q_omax = INT_MIN, q_dead = 0;
-  for (int w = 0; w < 4; ++w) {
-    q_dmin = min(q_dmin, bar->qsum[w][0]);
-    q_dmax = max(q_dmax, bar->qsum[w][1]);
-    q_omin = min(q_omin, bar->qsum[w][2]);
-    q_omax = max(q_omax, bar->qsum[w][3]);
-    q_dead |= bar->qsum[w][4];
-  }
   const int cnt = p.kv_cnt ? p.kv_cnt[item] : p.nk;
   const int32_t *kvrow = p.kv_idx ? p.kv_idx + item * p.nk : nullptr;
   const bool ragged = p.N % KB != 0;
@@ -247,25 +251,30 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int j0 = 0; j0 < cnt; j0 += kThreads) {
       const int j = j0 + tid;
       int kb = -1;
-      bool see = false, whole = true;
+      bool see = false;
+      uint32_t cls = 0;
       if (j < cnt) {
         kb = kvrow ? kvrow[j] : j;
         if (kb < 0 || kb >= p.nk) {
           bad = true;
         } else {
-          see = true;
-          if (masked) {
-            const int4 s = p.blocks[(long long)b * p.nk + kb];
+          int4 sum = make_int4(0, 0, 0, 0);
+          if (masked) sum = p.blocks[(long long)b * p.nk + kb];
+          const bool cut = ragged && kb == p.nk - 1;
+          for (int w = 0; w < active; ++w) {
+            bool some = true, whole = !cut;
+            const int *q = bar->qsum[w];
             if (p.q_doc) {
-              see = q_dmax >= 0 && s.y >= 0 && max(s.x, 0) <= q_dmax && s.y >= q_dmin;
-              whole = !q_dead && q_dmin == q_dmax && s.x == s.y && s.x == q_dmin;
+              some = q[1] >= 0 && sum.y >= 0 && max(sum.x, 0) <= q[1] && sum.y >= q[0];
+              whole = whole && !q[4] && q[0] == q[1] && sum.x == sum.y && sum.x == q[0];
             }
             if (p.q_order) {
-              see = see && s.z <= q_omax;
-              whole = whole && s.w <= q_omin;
+              some = some && sum.z <= q[3];
+              whole = whole && sum.w <= q[2];
             }
+            see |= some;
+            cls |= (some ? (whole ? kWhole : kMixed) : kNone) << (2 * w);
           }
-          if (ragged && kb == p.nk - 1) whole = false;
         }
       }
       const uint32_t seen = __ballot_sync(0xffffffffu, see);
@@ -277,7 +286,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (w < warp) at += n;
         kept += n;
       }
-      if (see) list[at + __popc(seen & ((1u << lane) - 1))] = (uint16_t)kb | (whole ? 0 : kPartial);
+      if (see) {
+        at += __popc(seen & ((1u << lane) - 1));
+        list[at] = (uint16_t)kb;
+        classes[at] = (uint8_t)cls;
+      }
       __syncthreads();
     }
   }
@@ -291,431 +304,554 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int first = (int)((long long)all_tiles * blockIdx.y / p.splits);
   const int tiles = any_bad ? 0 : (int)((long long)all_tiles * (blockIdx.y + 1) / p.splits) - first;
   if (any_bad && tid == 0) report_error(p.dev_err, RESS_ERR_DEVICE_BOUNDS);
-  // partial sums of a shared row
-  const long long slot = item * p.splits + blockIdx.y;
 
   if (tiles > 0) {
     const int entries = KB == 128 ? tiles : min(2 * tiles, kept - 2 * first);
-    const uint16_t *mine = list + (KB == 128 ? first : 2 * first);
-    if (warp == kProducerWarp) {
-      // ------------------------------------------------------------ TMA producer
-      if (lane == 0) {
-        tma_prefetch_desc(&tmQ);
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
-        mbar_arrive_expect_tx(&bar->q_full, kTile);
-        tma_load_3d(smem + kOffQ, &tmQ, &bar->q_full, 0, qi * 128, (int)bh);
-        // one 128-row box, or two 64-row boxes (row N, past the last token, reads as zero
-        // where the row has no second block)
-        auto load_tile = [&](const CUtensorMap *tm, unsigned char *dst, uint64_t *full, int j) {
-          mbar_arrive_expect_tx(full, kTile);
-          if constexpr (KB == 128) {
-            tma_load_3d(dst, tm, full, 0, (mine[j] & ~kPartial) * 128, (int)bh);
-          } else {
-            const int r1 = 2 * j + 1 < entries ? (mine[2 * j + 1] & ~kPartial) * 64 : p.N;
-            tma_load_3d(dst, tm, full, 0, (mine[2 * j] & ~kPartial) * 64, (int)bh);
-            tma_load_3d(dst + kTile / 2, tm, full, 0, r1, (int)bh);
-          }
-        };
-        auto load_k = [&](int j) {
-          const int s = j % kKStages;
-          load_tile(&tmK, smem + kOffK + s * kTile, &bar->k_full[s], j);
-        };
-        auto load_v = [&](int j) {
-          const int s = j % kVStages;
-          load_tile(&tmV, smem + kOffV + s * kTile, &bar->v_full[s], j);
-        };
-        int nk = min(tiles, kKStages), nv = min(tiles, kVStages);
-        for (int j = 0; j < nk; ++j) load_k(j);
-        for (int j = 0; j < nv; ++j) load_v(j);
-        for (int j = 0; j < tiles; ++j) {
-          if (j + kKStages < tiles) {
-            if (!mbar_wait(&bar->k_empty[j % kKStages], (j / kKStages) & 1, abort)) break;
-            load_k(j + kKStages);
-            nk = j + kKStages + 1;
-          }
-          if (j + kVStages < tiles) {
-            if (!mbar_wait(&bar->v_empty[j % kVStages], (j / kVStages) & 1, abort)) break;
-            load_v(j + kVStages);
-            nv = j + kVStages + 1;
-          }
-        }
-        if (*abort == 0 && (nk < tiles || nv < tiles)) {
-          report_error(p.dev_err, RESS_ERR_DEVICE_TIMEOUT);
-          *abort = 1;
-        }
-        // never leave the CTA with copies in flight
-        for (int j = max(0, nk - kKStages); j < nk; ++j)
-          mbar_wait(&bar->k_full[j % kKStages], (j / kKStages) & 1, nullptr);
-        for (int j = max(0, nv - kVStages); j < nv; ++j)
-          mbar_wait(&bar->v_full[j % kVStages], (j / kVStages) & 1, nullptr);
-        mbar_wait(&bar->q_full, 0, nullptr);
-      }
-    } else if (warp == kMmaWarp) {
-      // ------------------------------------------------------ tensor-core issuer
-      if (lane == 0) {
-        const uint32_t sQ = smem_u32(smem + kOffQ);
-        const uint32_t sK = smem_u32(smem + kOffK);
-        const uint32_t sV = smem_u32(smem + kOffV);
-        volatile int *o_init = &bar->o_init;
-        bool ok = mbar_wait(&bar->q_full, 0, abort);
-        tc_fence_after();
-        const uint64_t dq = smem_desc(sQ);
-        for (int j = 0; ok && j <= tiles; ++j) {
-          if (j < tiles) {
-            const int s = j % kKStages;
-            ok = mbar_wait(&bar->k_full[s], (j / kKStages) & 1, abort);
-            if (ok && j > 0) ok = mbar_wait(&bar->s_free, (j - 1) & 1, abort);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t dk = smem_desc(sK + s * kTile);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_ss(tmem + kColS, dq + 2 * k, dk + 2 * k, kIdescS, k > 0);
-            mma_commit(&bar->s_full);
-            mma_commit(&bar->k_empty[s]);
-          }
-          if (j > 0) {
-            const int jp = j - 1, sp = jp % kVStages;
-            ok = mbar_wait(&bar->p_full, jp & 1, abort);
-            if (ok) ok = mbar_wait(&bar->v_full[sp], (jp / kVStages) & 1, abort);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t dv = smem_desc(sV + sp * kTile);
-            const bool add = jp > 0 || *o_init != 0;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              mma_ts(tmem + kColO, tmem + kColP + 8 * k, dv + 128 * k, kIdescPV, (add || k > 0));
-              if (k == 3) mma_commit(&bar->o_half);
-            }
-            mma_commit(&bar->o_done);
-            mma_commit(&bar->v_empty[sp]);
-          }
-        }
-        if (!ok) {
-          report_error(p.dev_err, RESS_ERR_DEVICE_TIMEOUT);
-          *abort = 1;
-        }
-        // drain: every MMA issued above has finished before the CTA tears down
-        mma_commit(&bar->drain);
-        mbar_wait(&bar->drain, 0, nullptr);
-      }
-    } else if (warp < active) {
-      // ------------------------------------------------------------- softmax
-      const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
-      int *m_doc = reinterpret_cast<int *>(smem + kOffMeta) + warp * 3 * 128;
-      int *m_order = m_doc + 128;
-      float *m_pos = reinterpret_cast<float *>(m_doc + 256);
-      // positions relative to the row block's first query: exact small numbers
-      long long ref = 0;
-      int q_lo = 0, q_hi = 0;  // positions of the warp's queries
-      float row_pos = 0.f, slope = 0.f;
-      if constexpr (BIAS) {
-        const int32_t *qp = p.q_pos + (long long)b * p.Nq;
-        ref = qp[qi * 128];
-        const int mine_pos = qp[min(t, p.Nq - 1)];
-        q_lo = __reduce_min_sync(0xffffffffu, mine_pos);
-        q_hi = __reduce_max_sync(0xffffffffu, mine_pos);
-        row_pos = (float)(mine_pos - ref);
-        slope = -p.slopes[h] * kLog2e;
-      }
+    const int skip = KB == 128 ? first : 2 * first;
+    const uint16_t *mine = list + skip;
+    if (tid == 0) {
+      bar->b = b;
+      bar->bh = (int)bh;
+      bar->qi = qi;
+      bar->active = active;
+      bar->skip = skip;
+      bar->tiles = tiles;
+      bar->entries = entries;
+    }
+    __syncthreads();
+    // A second pass over the tiles follows only where hidden values that are not finite have
+    // to be kept out of the products; J counts tiles over both, for the barriers' phases.
+    int meets = 0;
+    for (int pass = 0;; ++pass) {
+      const int J0 = pass * tiles;
+      bool again = false;
       float m_run = kNoMax, l_run = 0.f;
       bool ok = true;
-      int scans = 0, scan_phase = 0;
-      for (int j = 0; j < tiles && ok; ++j) {
-        const int e0 = KB == 128 ? mine[j] : mine[2 * j];
-        const int e1 = KB == 128 ? e0 : (2 * j + 1 < entries ? mine[2 * j + 1] : -1);
-        const bool partial = ((e0 | e1) & kPartial) != 0;  // an absent block (-1) is partial
-        // key of column c, or -1
-        auto key_of = [&](int c) {
+      if (warp == kProducerWarp) {
+        // ---------------------------------------------------------- TMA producer
+        if (lane == 0) {
+          if (pass == 0) {
+            tma_prefetch_desc(&tmQ);
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+            mbar_arrive_expect_tx(&bar->q_full, kTile);
+            tma_load_3d(smem + kOffQ, &tmQ, &bar->q_full, 0, qi * 128, (int)bh);
+          }
+          // one 128-row box, or two 64-row boxes (row N, past the last token, reads as zero
+          // where the row has no second block)
+          auto load_tile = [&](const CUtensorMap *tm, unsigned char *dst, uint64_t *full, int j) {
+            mbar_arrive_expect_tx(full, kTile);
+            if constexpr (KB == 128) {
+              tma_load_3d(dst, tm, full, 0, mine[j] * 128, (int)bh);
+            } else {
+              const int r1 = 2 * j + 1 < entries ? mine[2 * j + 1] * 64 : p.N;
+              tma_load_3d(dst, tm, full, 0, mine[2 * j] * 64, (int)bh);
+              tma_load_3d(dst + kTile / 2, tm, full, 0, r1, (int)bh);
+            }
+          };
+          // tile j waits for its slot's last user, tile J - stages
+          auto load_k = [&](int j) {
+            const int J = J0 + j, s = J % kKStages;
+            if (J >= kKStages && !mbar_wait(&bar->k_empty[s], (J / kKStages - 1) & 1, abort)) return false;
+            load_tile(&tmK, smem + kOffK + s * kTile, &bar->k_full[s], j);
+            return true;
+          };
+          auto load_v = [&](int j) {
+            const int J = J0 + j, s = J % kVStages;
+            if (J >= kVStages && !mbar_wait(&bar->v_empty[s], (J / kVStages - 1) & 1, abort)) return false;
+            load_tile(&tmV, smem + kOffV + s * kTile, &bar->v_full[s], j);
+            return true;
+          };
+          int nk = 0, nv = 0;
+          while (nk < min(tiles, kKStages) && load_k(nk)) ++nk;
+          while (nv < min(tiles, kVStages) && load_v(nv)) ++nv;
+          for (int j = 0; j < tiles; ++j) {
+            if (j + kKStages < tiles) {
+              if (!load_k(j + kKStages)) break;
+              nk = j + kKStages + 1;
+            }
+            if (j + kVStages < tiles) {
+              if (!load_v(j + kVStages)) break;
+              nv = j + kVStages + 1;
+            }
+          }
+          if (*abort == 0 && (nk < tiles || nv < tiles)) {
+            report_error(p.dev_err, RESS_ERR_DEVICE_TIMEOUT);
+            *abort = 1;
+          }
+          // never leave the CTA with copies in flight
+          for (int j = max(0, nk - kKStages); j < nk; ++j)
+            mbar_wait(&bar->k_full[(J0 + j) % kKStages], ((J0 + j) / kKStages) & 1, nullptr);
+          for (int j = max(0, nv - kVStages); j < nv; ++j)
+            mbar_wait(&bar->v_full[(J0 + j) % kVStages], ((J0 + j) / kVStages) & 1, nullptr);
+          mbar_wait(&bar->q_full, 0, nullptr);
+        }
+      } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------- tensor-core issuer
+        if (lane == 0) {
+          const uint32_t sQ = smem_u32(smem + kOffQ);
+          const uint32_t sK = smem_u32(smem + kOffK);
+          const uint32_t sV = smem_u32(smem + kOffV);
+          volatile int *o_init = &bar->o_init;
+          ok = mbar_wait(&bar->q_full, 0, abort);
+          tc_fence_after();
+          const uint64_t dq = smem_desc(sQ);
+          for (int j = 0; ok && j <= tiles; ++j) {
+            const int J = J0 + j;
+            if (j < tiles) {
+              const int s = J % kKStages;
+              ok = mbar_wait(&bar->k_full[s], (J / kKStages) & 1, abort);
+              if (ok && J > 0) ok = mbar_wait(&bar->s_free, (J - 1) & 1, abort);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t dk = smem_desc(sK + s * kTile);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma_ss(tmem + kColS, dq + 2 * k, dk + 2 * k, kIdescS, k > 0);
+              mma_commit(&bar->s_full);
+              mma_commit(&bar->k_empty[s]);
+            }
+            if (j > 0) {
+              const int Jp = J - 1, sp = Jp % kVStages;
+              ok = mbar_wait(&bar->p_full, Jp & 1, abort);
+              if (ok) ok = mbar_wait(&bar->v_full[sp], (Jp / kVStages) & 1, abort);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t dv = smem_desc(sV + sp * kTile);
+              const bool add = j > 1 || *o_init != 0;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                mma_ts(tmem + kColO, tmem + kColP + 8 * k, dv + 128 * k, kIdescPV, (add || k > 0));
+                if (k == 3) mma_commit(&bar->o_half);
+              }
+              mma_commit(&bar->o_done);
+              mma_commit(&bar->v_empty[sp]);
+            }
+          }
+          if (!ok) {
+            report_error(p.dev_err, RESS_ERR_DEVICE_TIMEOUT);
+            *abort = 1;
+          }
+          // drain: every MMA issued above has finished before the CTA tears down
+          mma_commit(&bar->drain);
+          mbar_wait(&bar->drain, pass & 1, nullptr);
+        }
+      } else if (warp < active) {
+        // ----------------------------------------------------------- softmax
+        const volatile Bars *vb = bar;
+        const uint32_t trow = vb->tmem_base + ((uint32_t)(warp * 32) << 16);
+        int *m_doc = reinterpret_cast<int *>(smem + kOffMeta), *m_order = m_doc + 128;
+        float *m_pos = reinterpret_cast<float *>(smem + kOffPos) + warp * 128;
+        // positions relative to the row block's first query: exact small numbers
+        int ref = 0, q_lo = 0, q_hi = 0;  // and the range of the warp's queries
+        float row_pos = 0.f, slope = 0.f;
+        int4 pos[KB == 64 ? 2 : 1];  // position summaries of the next tile's blocks
+        if constexpr (BIAS) {
+          const int32_t *qp = p.q_pos + (long long)vb->b * p.Nq;
+          ref = qp[vb->qi * 128];
+          const int mine_pos = qp[min(vb->qi * 128 + tid, p.Nq - 1)];
+          q_lo = __reduce_min_sync(0xffffffffu, mine_pos);
+          q_hi = __reduce_max_sync(0xffffffffu, mine_pos);
+          row_pos = (float)((long long)mine_pos - ref);
+          slope = -p.slopes[vb->bh % p.H] * kLog2e;
+        }
+        // key of column c of tile j, or -1
+        auto key_of = [&](int j, int c) {
+          const volatile uint16_t *own = list + vb->skip;
           int u;
           if constexpr (KB == 128) {
-            u = (e0 & ~kPartial) * 128 + c;
+            u = own[j] * 128 + c;
           } else {
-            if (c >= 64 && e1 < 0) return -1;
-            u = ((c < 64 ? e0 : e1) & 0x7fff) * 64 + (c & 63);
+            if (c >= 64 && 2 * j + 1 >= vb->entries) return -1;
+            u = own[2 * j + (c >> 6)] * 64 + (c & 63);
           }
           return u < p.N ? u : -1;
         };
-        // +1: every key lies at or before every query of the warp, -1: at or after, 0: mixed
-        int side = 0;
-        bool gaps = false;  // columns without a key
-        if (BIAS || partial) {
-          __syncwarp();  // the last tile's values have been read
-          int pos[4], lo = INT_MAX, hi = INT_MIN;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = lane + 32 * i, u = key_of(c);
-            const long long at = (long long)b * p.N + u;
-            if constexpr (BIAS) {
-              pos[i] = u >= 0 ? __ldg(p.k_pos + at) : (int)ref;
-              if (u >= 0) {
-                lo = min(lo, pos[i]);
-                hi = max(hi, pos[i]);
-              }
-            }
-            gaps |= u < 0;
-            if (partial) {
+        auto load_pos = [&](int j) {
+          const volatile uint16_t *own = list + vb->skip;
+          const int4 *sum = p.blocks + (long long)(p.B + vb->b) * p.nk;
+          if constexpr (KB == 128) {
+            pos[0] = __ldg(sum + own[j]);
+          } else {
+            pos[0] = __ldg(sum + own[2 * j]);
+            if (2 * j + 1 < vb->entries) pos[1] = __ldg(sum + own[2 * j + 1]);
+            else pos[1] = pos[0];
+          }
+        };
+        // the softmax warps meet (a bounded wait, as all others)
+        auto meet = [&]() {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->meet);
+          const bool there = warp_wait(&bar->meet, meets & 1, abort);
+          ++meets;
+          return there;
+        };
+        if constexpr (BIAS) load_pos(0);
+        for (int j = 0; j < vb->tiles; ++j) {
+          const int J = (pass ? vb->tiles : 0) + j;
+          // the warps' classes of this tile: of its block, or of its two
+          const volatile uint8_t *own = classes + vb->skip + (KB == 128 ? j : 2 * j);
+          uint32_t cls = own[0];
+          if constexpr (KB == 64) {
+            const uint32_t c1 = 2 * j + 1 < vb->entries ? own[1] : 0xAAu;
+            const uint32_t differ = ((cls ^ c1) | ((cls ^ c1) >> 1)) & 0x55u;
+            cls = (cls & ~(3u * differ)) | differ;
+          }
+          cls &= (1u << (2 * vb->active)) - 1;
+          const uint32_t code = (cls >> (2 * warp)) & 3;
+          if (cls & ~(cls >> 1) & 0x55u) {  // mixed for some warp
+            ok = meet();  // the last mixed tile's arrays have been read
+            if (!ok) break;
+            for (int c = tid; c < 128; c += 32 * vb->active) {
+              const int u = key_of(j, c);
+              const long long at = (long long)vb->b * p.N + u;
               m_doc[c] = u < 0 ? -1 : (p.k_doc ? max(__ldg(p.k_doc + at), -1) : 0);
               m_order[c] = u < 0 || !p.k_order ? 0 : __ldg(p.k_order + at);
             }
+            ok = meet();
+            if (!ok) break;
           }
+          // The bias of column c of half i, where the keys lie on one side of the warp's
+          // queries: shift[i] + step[i] (c mod 64) if positions run evenly in each half (the
+          // usual case: tokens, or all of one view), else shift[i] + m_pos[c].
+          float shift[2] = {0.f, 0.f}, step[2] = {0.f, 0.f};
+          int side = 0;  // +1: every key at or before every query, -1: at or after, 0: mixed
+          bool even = true;
           if constexpr (BIAS) {
-            lo = __reduce_min_sync(0xffffffffu, lo);
-            hi = __reduce_max_sync(0xffffffffu, hi);
+            const int4 p0 = pos[0], p1 = pos[KB == 64 ? 1 : 0];  // smallest, largest, first, step
+            const int lo = min(p0.x, p1.x), hi = max(p0.y, p1.y);
             side = hi <= q_lo ? 1 : (lo >= q_hi ? -1 : 0);
-            // on one side the bias is a term of the row plus one of the column
+            even = side != 0 && p0.w != kUneven && p1.w != kUneven;
             const float f = side == 0 ? 1.0f : (side > 0 ? -slope : slope);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m_pos[lane + 32 * i] = (float)(pos[i] - ref) * f;
-          }
-          gaps = __any_sync(0xffffffffu, gaps);
-          __syncwarp();
-        }
-        ok = warp_wait(&bar->s_full, j & 1, abort);
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t sv[128];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          tmem_ld32(trow + kColS + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * i]));
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->s_free);
-        // z = sv * sc + shift from here on
-        float sc = p.scale_log2, shift = 0.f;
-        if constexpr (CAP) {
-          float mc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < 128; c += 8) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              mc[q] = fmax3(mc[q], fabsf(__uint_as_float(sv[c + 2 * q])), fabsf(__uint_as_float(sv[c + 2 * q + 1])));
-          }
-          const float big = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
-          if (__all_sync(0xffffffffu, big <= p.cap_half))
-            cap_small<4>(sv, p.cap_in);
-          else if (__all_sync(0xffffffffu, big <= 2.0f * p.cap_half))
-            cap_small<6>(sv, p.cap_in);
-          else
-            cap_any(sv, p.cap_in);
-          sc = p.cap_log2;
-        }
-        if constexpr (BIAS) {
-          if (side != 0) {
-            shift = (side > 0 ? slope : -slope) * row_pos;
-            const uint64_t sc2 = f2(sc, sc);
-#pragma unroll
-            for (int c = 0; c < 128; c += 4) {
-              const ulonglong2 kp = *reinterpret_cast<const ulonglong2 *>(m_pos + c);
-              const uint64_t z0 = ffma2(f2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sc2, kp.x);
-              const uint64_t z1 = ffma2(f2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), sc2, kp.y);
-              sv[c] = (uint32_t)z0;
-              sv[c + 1] = (uint32_t)(z0 >> 32);
-              sv[c + 2] = (uint32_t)z1;
-              sv[c + 3] = (uint32_t)(z1 >> 32);
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 128; c += 4) {
-              const float4 kp = *reinterpret_cast<const float4 *>(m_pos + c);
-              const float d[4] = {fabsf(row_pos - kp.x), fabsf(row_pos - kp.y), fabsf(row_pos - kp.z),
-                                  fabsf(row_pos - kp.w)};
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                sv[c + i] = __float_as_uint(fmaf(slope, d[i], __uint_as_float(sv[c + i]) * sc));
+            if (even) {
+              step[0] = f * (float)p0.w;
+              step[1] = f * (float)p1.w;
+              shift[0] = f * ((float)((long long)p0.z - ref) - row_pos);
+              shift[1] = KB == 64 ? f * ((float)((long long)p1.z - ref) - row_pos) : fmaf(64.0f, step[0], shift[0]);
+            } else {
+              shift[0] = shift[1] = side == 0 ? 0.f : -f * row_pos;
+              __syncwarp();  // the last tile's have been read
+              for (int c = lane; c < 128; c += 32) {
+                const int u = max(key_of(j, c), 0);  // (a column without a key is masked)
+                m_pos[c] = (float)((long long)__ldg(p.k_pos + (long long)vb->b * p.N + u) - ref) * f;
+              }
+              __syncwarp();
             }
           }
-          sc = 1.0f;
-        }
-        if (partial) {
-          if (p.q_doc || gaps) {
-#pragma unroll
-            for (int c = 0; c < 128; c += 4) {
-              const int4 kd = *reinterpret_cast<const int4 *>(m_doc + c);
-              if (kd.x != row_doc) sv[c] = __float_as_uint(-INFINITY);
-              if (kd.y != row_doc) sv[c + 1] = __float_as_uint(-INFINITY);
-              if (kd.z != row_doc) sv[c + 2] = __float_as_uint(-INFINITY);
-              if (kd.w != row_doc) sv[c + 3] = __float_as_uint(-INFINITY);
-            }
-          }
-          if (p.q_order) {
-#pragma unroll
-            for (int c = 0; c < 128; c += 4) {
-              const int4 ko = *reinterpret_cast<const int4 *>(m_order + c);
-              if (ko.x > row_order) sv[c] = __float_as_uint(-INFINITY);
-              if (ko.y > row_order) sv[c + 1] = __float_as_uint(-INFINITY);
-              if (ko.z > row_order) sv[c + 2] = __float_as_uint(-INFINITY);
-              if (ko.w > row_order) sv[c + 3] = __float_as_uint(-INFINITY);
-            }
-          }
-        }
-        // values of a partial tile that are not finite: which rows of V hold one
-        uint32_t vbad[4] = {0, 0, 0, 0};
-        const int sp = j % kVStages;
-        const bool scan = masked && partial;
-        if (scan) {
-          ok = warp_wait(&bar->v_full[sp], (j / kVStages) & 1, abort);
-          if (!ok) break;
-          for (int r = warp; r < 4; r += active) {
-            const uint4 *vr = reinterpret_cast<const uint4 *>(smem + kOffV + sp * kTile + (32 * r + lane) * 128);
-            bool inf = false;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint4 w = vr[(i + lane) & 7];
-              for (uint32_t y : {w.x, w.y, w.z, w.w})
-                inf |= (y & 0x7f80u) == 0x7f80u || (y & 0x7f800000u) == 0x7f800000u;
-            }
-            const uint32_t bits = __ballot_sync(0xffffffffu, inf);
-            if (lane == 0) *reinterpret_cast<volatile uint32_t *>(&bar->vflag[scans & 1][r]) = bits;
-          }
-          if (lane == 0) mbar_arrive(&bar->scan);
-          ok = warp_wait(&bar->scan, scan_phase & 1, abort);
-          if (!ok) break;
-          ++scan_phase;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) vbad[i] = *reinterpret_cast<volatile uint32_t *>(&bar->vflag[scans & 1][i]);
-          ++scans;
-        }
-        const bool by_hand = (vbad[0] | vbad[1] | vbad[2] | vbad[3]) != 0;
-        // row max
-        float mc[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mc[q] = fmaxf(__uint_as_float(sv[2 * q]), __uint_as_float(sv[2 * q + 1]));
-#pragma unroll
-        for (int c = 8; c < 128; c += 8) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            mc[q] = fmax3(mc[q], __uint_as_float(sv[c + 2 * q]), __uint_as_float(sv[c + 2 * q + 1]));
-        }
-        const float mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
-        const float m_new = fmaxf(m_run, fmaf(mx, sc, shift));
-        const bool rescale = m_new > m_run + kRescaleLog2;
-        const float m_use = rescale ? m_new : m_run;
-        const float alpha = rescale ? ex2_approx(m_run - m_new) : 1.0f;
-        const uint64_t sc2 = f2(sc, sc);
-        const uint64_t nm2 = f2(shift - m_use, shift - m_use);
-        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-        uint32_t pk[64];
-#pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          const uint64_t s2 = f2(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1]));
-          const uint64_t z = BIAS ? fadd2(s2, nm2) : ffma2(s2, sc2, nm2);
-          const uint64_t e = f2(ex2_approx(f2lo(z)), ex2_approx(f2hi(z)));
-          acc[c & 3] = fadd2(acc[c & 3], e);
-          pk[c] = pack_bf16x2(f2lo(e), f2hi(e));
-          if (c == 31) {
-            // keys 0..63 of P: free once the first half of the previous product is done
-            if (j > 0) ok = warp_wait(&bar->o_half, (j - 1) & 1, abort);
-            if (ok) tmem_st32(trow + kColP, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-          }
-        }
-        if (!ok) break;
-        const uint64_t a = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
-        l_run = l_run * alpha + (f2lo(a) + f2hi(a));
-        if (j > 0) {
-          ok = warp_wait(&bar->o_done, (j - 1) & 1, abort);
+          ok = warp_wait(&bar->s_full, J & 1, abort);
           if (!ok) break;
           tc_fence_after();
-          if (__any_sync(0xffffffffu, rescale)) {
-            uint32_t ov[32];
+          uint32_t sv[128];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              tmem_ld32(trow + kColO + 32 * i, ov);
-              tmem_wait_ld();
+          for (int i = 0; i < 4; ++i)
+            tmem_ld32(trow + kColS + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * i]));
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->s_free);
+          bool rescale = false;
+          float alpha = 1.0f, m_use = m_run;
+          uint32_t pk[64];
+          // P and its sum from the exponents of column pairs
+          auto weights = [&](auto z_of) {
+            alpha = rescale ? ex2_approx(m_run - m_use) : 1.0f;
+            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-              for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha);
-              tmem_st32(trow + kColO + 32 * i, ov);
-            }
-          }
-        }
-        tmem_st32(trow + kColP + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
-        tmem_wait_st();
-        if (by_hand) {
-          // values that are not finite go to the rows that see them, and out of the tile
-          unsigned char *vt = smem + kOffV + sp * kTile;
-          uint32_t ov[32];
-#pragma unroll 1
-          for (int i = 0; i < 2; ++i) {
-            if (j > 0) {
-              tmem_ld32(trow + kColO + 32 * i, ov);
-              tmem_wait_ld();
-            } else {
-#pragma unroll
-              for (int c = 0; c < 32; ++c) ov[c] = 0;
-            }
-#pragma unroll 1
-            for (int u = 0; u < 128; ++u) {
-              const uint32_t word = u < 32 ? vbad[0] : (u < 64 ? vbad[1] : (u < 96 ? vbad[2] : vbad[3]));
-              if (!(word >> (u & 31) & 1) || m_doc[u] != row_doc || m_order[u] > row_order) continue;
-#pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                const int d = 32 * i + c;
-                const uint32_t bits = *reinterpret_cast<const uint16_t *>(
-                    vt + u * 128 + (((d >> 3) ^ (u & 7)) << 4) + (d & 7) * 2);
-                if ((bits & 0x7f80u) == 0x7f80u)
-                  ov[c] = __float_as_uint(__uint_as_float(ov[c]) + __uint_as_float(bits << 16));
+            for (int c = 0; c < 64; ++c) {
+              const uint64_t z = z_of(c);
+              const uint64_t e = f2(ex2_approx(f2lo(z)), ex2_approx(f2hi(z)));
+              acc[c & 3] = fadd2(acc[c & 3], e);
+              pk[c] = pack_bf16x2(f2lo(e), f2hi(e));
+              if (c == 31) {
+                // keys 0..63 of P: free once the first half of the previous product is done
+                if (j > 0) ok = warp_wait(&bar->o_half, (J - 1) & 1, abort);
+                if (ok) tmem_st32(trow + kColP, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
               }
             }
-            __syncwarp();
-            tmem_st32(trow + kColO + 32 * i, ov);
+            const uint64_t a = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+            l_run = l_run * alpha + (f2lo(a) + f2hi(a));
+            m_run = m_use;
+          };
+          auto raise = [&](float m_new) {
+            rescale = m_new > m_run + kRescaleLog2;
+            m_use = rescale ? m_new : m_run;
+          };
+          float big = 0.f;  // largest |score|, for the cap
+          bool fused = false;
+          if constexpr (CAP) {
+            float mc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 128; c += 8) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                mc[q] = fmax3(mc[q], fabsf(__uint_as_float(sv[c + 2 * q])), fabsf(__uint_as_float(sv[c + 2 * q + 1])));
+            }
+            big = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
+            fused = !BIAS && code == kWhole && __all_sync(0xffffffffu, big <= p.cap_a);
           }
-          tmem_wait_st();
-          if (lane == 0) {
-            if (j == 0) *reinterpret_cast<volatile int *>(&bar->o_init) = 1;
-            mbar_arrive(&bar->scan);
+          if (code == kNone) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) pk[c] = 0u;
+            if (j > 0) ok = warp_wait(&bar->o_half, (J - 1) & 1, abort);
+            if (ok) tmem_st32(trow + kColP, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+          } else if (CAP && !BIAS && fused) {
+            // the cap inside the exponent, s P(s^2) with the scales in its coefficients; the
+            // cap of the largest |s| bounds the row's scores
+            const float y = big * big;
+            raise(fmaxf(m_run, big * fmaf(fmaf(fmaf(p.cap_k[3], y, p.cap_k[2]), y, p.cap_k[1]), y, p.cap_k[0])));
+            const uint64_t k0 = f2(p.cap_k[0], p.cap_k[0]), k1 = f2(p.cap_k[1], p.cap_k[1]);
+            const uint64_t k2 = f2(p.cap_k[2], p.cap_k[2]), k3 = f2(p.cap_k[3], p.cap_k[3]);
+            const uint64_t nm = f2(-m_use, -m_use);
+            weights([&](int c) {
+              const uint64_t s2 = f2(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1]));
+              const uint64_t t = fmul2(s2, s2);
+              return ffma2(ffma2(ffma2(ffma2(k3, t, k2), t, k1), t, k0), s2, nm);
+            });
+          } else {
+            // z = sv * sc + shift from here on
+            float sc = p.scale_log2;
+            if constexpr (CAP) {
+              if (__all_sync(0xffffffffu, big <= p.cap_half))
+                cap_small<4>(sv, p.cap_in);
+              else if (__all_sync(0xffffffffu, big <= 2.0f * p.cap_half))
+                cap_small<6>(sv, p.cap_in);
+              else
+                cap_any(sv, p.cap_in);
+              sc = p.cap_log2;
+            }
+            if constexpr (BIAS) {
+              const uint64_t sc2 = f2(sc, sc);
+              if (!even || step[0] != 0.f || step[1] != 0.f) {
+                if (even) {
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    const uint64_t st = f2(8.0f * step[i], 8.0f * step[i]);
+                    uint64_t run[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) run[q] = f2(2 * q * step[i], (2 * q + 1) * step[i]);
+#pragma unroll
+                    for (int c = 64 * i; c < 64 * i + 64; c += 2) {
+                      const int q = (c >> 1) & 3;
+                      const uint64_t z = ffma2(f2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sc2, run[q]);
+                      run[q] = fadd2(run[q], st);
+                      sv[c] = (uint32_t)z;
+                      sv[c + 1] = (uint32_t)(z >> 32);
+                    }
+                  }
+                } else if (side != 0) {
+#pragma unroll
+                  for (int c = 0; c < 128; c += 4) {
+                    const ulonglong2 kp = *reinterpret_cast<const ulonglong2 *>(m_pos + c);
+                    const uint64_t z0 = ffma2(f2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sc2, kp.x);
+                    const uint64_t z1 = ffma2(f2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), sc2, kp.y);
+                    sv[c] = (uint32_t)z0;
+                    sv[c + 1] = (uint32_t)(z0 >> 32);
+                    sv[c + 2] = (uint32_t)z1;
+                    sv[c + 3] = (uint32_t)(z1 >> 32);
+                  }
+                } else {
+#pragma unroll
+                  for (int c = 0; c < 128; c += 4) {
+                    const float4 kp = *reinterpret_cast<const float4 *>(m_pos + c);
+                    const float d[4] = {fabsf(row_pos - kp.x), fabsf(row_pos - kp.y), fabsf(row_pos - kp.z),
+                                        fabsf(row_pos - kp.w)};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                      sv[c + i] = __float_as_uint(fmaf(slope, d[i], __uint_as_float(sv[c + i]) * sc));
+                  }
+                }
+                sc = 1.0f;
+              }
+            }
+            if (code == kMixed) {
+              const int t = vb->qi * 128 + tid;
+              {
+                int row_doc = 0;  // (a column without a key has document -1)
+                if (p.q_doc) row_doc = t < p.Nq ? __ldg(p.q_doc + (long long)vb->b * p.Nq + t) : -1;
+                if (row_doc < 0) row_doc = -2;  // equal to no key's document
+#pragma unroll
+                for (int c = 0; c < 128; c += 4) {
+                  const int4 kd = *reinterpret_cast<const int4 *>(m_doc + c);
+                  if (kd.x != row_doc) sv[c] = __float_as_uint(-INFINITY);
+                  if (kd.y != row_doc) sv[c + 1] = __float_as_uint(-INFINITY);
+                  if (kd.z != row_doc) sv[c + 2] = __float_as_uint(-INFINITY);
+                  if (kd.w != row_doc) sv[c + 3] = __float_as_uint(-INFINITY);
+                }
+              }
+              if (p.q_order) {
+                const int row_order = t < p.Nq ? __ldg(p.q_order + (long long)vb->b * p.Nq + t) : 0;
+#pragma unroll
+                for (int c = 0; c < 128; c += 4) {
+                  const int4 ko = *reinterpret_cast<const int4 *>(m_order + c);
+                  if (ko.x > row_order) sv[c] = __float_as_uint(-INFINITY);
+                  if (ko.y > row_order) sv[c + 1] = __float_as_uint(-INFINITY);
+                  if (ko.z > row_order) sv[c + 2] = __float_as_uint(-INFINITY);
+                  if (ko.w > row_order) sv[c + 3] = __float_as_uint(-INFINITY);
+                }
+              }
+            }
+            float mh[2];  // maxima of the halves
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float mc[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+              for (int c = 64 * i; c < 64 * i + 64; c += 4) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                  mc[q] = fmax3(mc[q], __uint_as_float(sv[c + 2 * q]), __uint_as_float(sv[c + 2 * q + 1]));
+              }
+              mh[i] = fmaxf(mc[0], mc[1]);
+            }
+            if constexpr (BIAS)
+              raise(fmax3(m_run, fmaf(mh[0], sc, shift[0]), fmaf(mh[1], sc, shift[1])));
+            else
+              raise(fmaxf(m_run, fmaxf(mh[0], mh[1]) * sc));
+            const uint64_t sc2 = f2(sc, sc);
+            const uint64_t n0 = f2(shift[0] - m_use, shift[0] - m_use), n1 = f2(shift[1] - m_use, shift[1] - m_use);
+            weights([&](int c) {
+              const uint64_t s2 = f2(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1]));
+              return ffma2(s2, sc2, c < 32 ? n0 : n1);
+            });
           }
-          ok = warp_wait(&bar->scan, scan_phase & 1, abort);
           if (!ok) break;
-          ++scan_phase;
-          for (int r = warp; r < 4; r += active) {
-            uint16_t *vr = reinterpret_cast<uint16_t *>(vt + (32 * r + lane) * 128);
-#pragma unroll 1
-            for (int c = 0; c < 64; ++c)
-              if ((vr[c] & 0x7f80u) == 0x7f80u) vr[c] = 0;
+          if constexpr (BIAS)
+            if (j + 1 < tiles) load_pos(j + 1);
+          if (j > 0) {
+            ok = warp_wait(&bar->o_done, (J - 1) & 1, abort);
+            if (!ok) break;
+            tc_fence_after();
+            if (__any_sync(0xffffffffu, rescale)) {
+              uint32_t ov[32];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                tmem_ld32(trow + kColO + 32 * i, ov);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha);
+                tmem_st32(trow + kColO + 32 * i, ov);
+              }
+            }
           }
-          fence_async_shared();
+          tmem_st32(trow + kColP + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+          tmem_wait_st();
+          if (pass == 1 && cls != 0) {
+            // which rows of V hold a value that is not finite
+            const int sp = J % kVStages;
+            unsigned char *vt = smem + kOffV + sp * kTile;
+            ok = warp_wait(&bar->v_full[sp], (J / kVStages) & 1, abort);
+            if (!ok) break;
+            for (int r = warp; r < 4; r += vb->active) {
+              const uint32_t *vr = reinterpret_cast<const uint32_t *>(vt + (32 * r + lane) * 128);
+              bool inf = false;
+#pragma unroll 1
+              for (int i = 0; i < 32; ++i) {
+                const uint32_t y = vr[(i + lane) & 31];
+                inf |= (y & 0x7f80u) == 0x7f80u || (y & 0x7f800000u) == 0x7f800000u;
+              }
+              const uint32_t bits = __ballot_sync(0xffffffffu, inf);
+              if (lane == 0) *reinterpret_cast<volatile uint32_t *>(&bar->vflag[r]) = bits;
+            }
+            ok = meet();
+            if (!ok) break;
+            const volatile uint32_t *vbad = bar->vflag;
+            if ((vbad[0] | vbad[1] | vbad[2] | vbad[3]) != 0) {
+              // they go to the rows that see them, and out of the tile
+              const int t = vb->qi * 128 + tid;
+              const bool there = t < p.Nq;
+              int row_doc = 0, row_order = 0;
+              if (p.q_doc) row_doc = there ? __ldg(p.q_doc + (long long)vb->b * p.Nq + t) : -1;
+              if (p.q_order) row_order = there ? __ldg(p.q_order + (long long)vb->b * p.Nq + t) : 0;
+              if (row_doc < 0) row_doc = -2;
+              uint32_t ov[32];
+#pragma unroll 1
+              for (int i = 0; i < 2; ++i) {
+                if (j > 0) {
+                  tmem_ld32(trow + kColO + 32 * i, ov);
+                  tmem_wait_ld();
+                } else {
+#pragma unroll
+                  for (int c = 0; c < 32; ++c) ov[c] = 0;
+                }
+#pragma unroll 1
+                for (int u = 0; u < 128; ++u) {
+                  if (!(vbad[u >> 5] >> (u & 31) & 1) || code == kNone) continue;
+                  if (code == kMixed && (m_doc[u] != row_doc || m_order[u] > row_order)) continue;
+#pragma unroll
+                  for (int c = 0; c < 32; ++c) {
+                    const int d = 32 * i + c;
+                    const uint32_t bits = *reinterpret_cast<const uint16_t *>(
+                        vt + u * 128 + (((d >> 3) ^ (u & 7)) << 4) + (d & 7) * 2);
+                    if ((bits & 0x7f80u) == 0x7f80u)
+                      ov[c] = __float_as_uint(__uint_as_float(ov[c]) + __uint_as_float(bits << 16));
+                  }
+                }
+                __syncwarp();
+                tmem_st32(trow + kColO + 32 * i, ov);
+              }
+              tmem_wait_st();
+              if (j == 0 && lane == 0) *reinterpret_cast<volatile int *>(&bar->o_init) = 1;
+              ok = meet();
+              if (!ok) break;
+              for (int r = warp; r < 4; r += vb->active) {
+                uint16_t *vr = reinterpret_cast<uint16_t *>(vt + (32 * r + lane) * 128);
+#pragma unroll 1
+                for (int c = 0; c < 64; ++c)
+                  if ((vr[c] & 0x7f80u) == 0x7f80u) vr[c] = 0;
+              }
+              fence_async_shared();
+            }
+            ok = meet();  // the flags have been read
+            if (!ok) break;
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->p_full);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->p_full);
-        m_run = m_use;
-      }
-      if (ok) ok = warp_wait(&bar->o_done, (tiles - 1) & 1, abort);
-      if (!ok) {
-        report_error(p.dev_err, RESS_ERR_DEVICE_TIMEOUT);
-        *abort = 1;
-        if (p.splits > 1 && t < p.Nq) p.part_ml[slot * 128 + tid] = make_float2(0.f, -1.f);
-      } else {
-        tc_fence_after();
-        uint32_t o[64];
-        tmem_ld32(trow + kColO, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
-        tmem_ld32(trow + kColO + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
-        tmem_wait_ld();
-        if (t < p.Nq && p.splits > 1) {
-          p.part_ml[slot * 128 + tid] = make_float2(m_run, l_run);
-          uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + (slot * 128 + tid) * 64);
+        const int t = vb->qi * 128 + tid;
+        const long long slot = ((long long)vb->bh * p.nq + vb->qi) * p.splits + blockIdx.y;
+        if (ok) ok = warp_wait(&bar->o_done, ((pass + 1) * vb->tiles - 1) & 1, abort);
+        if (!ok) {
+          report_error(p.dev_err, RESS_ERR_DEVICE_TIMEOUT);
+          *abort = 1;
+          if (p.splits > 1 && t < p.Nq) p.part_ml[slot * 128 + tid] = make_float2(0.f, -1.f);
+        } else {
+          tc_fence_after();
+          uint32_t o[64];
+          tmem_ld32(trow + kColO, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
+          tmem_ld32(trow + kColO + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
+          tmem_wait_ld();
+          if (masked && pass == 0 && t < p.Nq && l_run != 0.f) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-        } else if (t < p.Nq) {
-          // a row that saw no key is zero whatever the products hold
-          const bool none = l_run == 0.f;
-          const float inv = 1.0f / l_run;
-          uint32_t w[32];
+            for (int c = 0; c < 64; ++c) again |= (o[c] & 0x7f800000u) == 0x7f800000u;
+          }
+          if (t < p.Nq && p.splits > 1) {
+            p.part_ml[slot * 128 + tid] = make_float2(m_run, l_run);
+            uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + (slot * 128 + tid) * 64);
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            w[c] = none ? 0u : pack_bf16x2(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv);
-          uint4 *dst = reinterpret_cast<uint4 *>(p.out + ((size_t)bh * p.Nq + t) * 64);
+            for (int c = 0; c < 16; ++c) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+          } else if (t < p.Nq) {
+            // a row that saw no key is zero whatever the products hold
+            const bool none = l_run == 0.f;
+            const float inv = 1.0f / l_run;
+            uint32_t w[32];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) dst[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-          if (p.lse)
-            p.lse[(size_t)bh * p.Nq + t] = none ? -INFINITY : (m_run + __log2f(l_run)) * kLn2;
+            for (int c = 0; c < 32; ++c)
+              w[c] = none ? 0u : pack_bf16x2(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv);
+            uint4 *dst = reinterpret_cast<uint4 *>(p.out + ((size_t)vb->bh * p.Nq + t) * 64);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) dst[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+            if (p.lse)
+              p.lse[(size_t)vb->bh * p.Nq + t] = none ? -INFINITY : (m_run + __log2f(l_run)) * kLn2;
+          }
         }
       }
+      if (!masked || pass == 1) break;
+      tc_fence_before();
+      if (!__syncthreads_or(again)) break;
+      tc_fence_after();
     }
   } else if (warp < 4 && t < p.Nq) {
     if (p.splits > 1) {
-      p.part_ml[slot * 128 + tid] = make_float2(kNoMax, any_bad ? -1.f : 0.f);
+      p.part_ml[(item * p.splits + blockIdx.y) * 128 + tid] = make_float2(kNoMax, any_bad ? -1.f : 0.f);
     } else if (!any_bad) {
       // nothing to see: zero rows
       uint4 *dst = reinterpret_cast<uint4 *>(p.out + ((size_t)bh * p.Nq + t) * 64);
@@ -771,28 +907,49 @@ __global__ void __launch_bounds__(256) join_kernel(const float *__restrict__ par
 }
 
 // ------------------------------------------------------------------- block summaries
-// One warp per key block: {min doc, max doc, min order, max order} over its tokens.
+// One warp per key block, over its tokens: {min doc, max doc, min order, max order}, and
+// {min, max, first position, step} with the step kUneven unless every position is first +
+// step * place.
 __global__ void __launch_bounds__(256) summary_kernel(const int32_t *__restrict__ doc,
-                                                      const int32_t *__restrict__ order, int N, int nk,
-                                                      int kb, long long blocks, int4 *__restrict__ out) {
+                                                      const int32_t *__restrict__ order,
+                                                      const int32_t *__restrict__ pos, int N, int nk, int kb,
+                                                      long long blocks, int4 *__restrict__ out) {
   const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (i >= blocks) return;
   const long long b = i / nk;
-  const int j = (int)(i - b * nk);
-  int4 s = make_int4(INT_MAX, INT_MIN, INT_MAX, INT_MIN);
-  for (int u = j * kb + lane; u < min(N, (j + 1) * kb); u += 32) {
-    const int d = doc ? doc[b * N + u] : 0, o = order ? order[b * N + u] : 0;
-    s.x = min(s.x, d);
-    s.y = max(s.y, d);
-    s.z = min(s.z, o);
-    s.w = max(s.w, o);
+  const int j = (int)(i - b * nk), u0 = j * kb, n = min(N - u0, kb);
+  if (doc || order) {
+    int4 s = make_int4(INT_MAX, INT_MIN, INT_MAX, INT_MIN);
+    for (int u = lane; u < n; u += 32) {
+      const int d = doc ? doc[b * N + u0 + u] : 0, o = order ? order[b * N + u0 + u] : 0;
+      s.x = min(s.x, d);
+      s.y = max(s.y, d);
+      s.z = min(s.z, o);
+      s.w = max(s.w, o);
+    }
+    s.x = __reduce_min_sync(0xffffffffu, s.x);
+    s.y = __reduce_max_sync(0xffffffffu, s.y);
+    s.z = __reduce_min_sync(0xffffffffu, s.z);
+    s.w = __reduce_max_sync(0xffffffffu, s.w);
+    if (lane == 0) out[i] = s;
   }
-  s.x = __reduce_min_sync(0xffffffffu, s.x);
-  s.y = __reduce_max_sync(0xffffffffu, s.y);
-  s.z = __reduce_min_sync(0xffffffffu, s.z);
-  s.w = __reduce_max_sync(0xffffffffu, s.w);
-  if (lane == 0) out[i] = s;
+  if (pos) {
+    pos += b * N + u0;
+    int lo = INT_MAX, hi = INT_MIN;
+    const long long first = pos[0], step = n > 1 ? pos[1] - first : 0;
+    bool even = step > -(1 << 20) && step < (1 << 20);
+    for (int u = lane; u < n; u += 32) {
+      const int x = pos[u];
+      lo = min(lo, x);
+      hi = max(hi, x);
+      even = even && x == first + step * u;
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    even = __all_sync(0xffffffffu, even);
+    if (lane == 0) out[blocks + i] = make_int4(lo, hi, (int)first, even ? (int)step : kUneven);
+  }
 }
 
 // Rows of a problem without keys: zero, and lse = -inf.
@@ -828,7 +985,7 @@ KernelFn pick(bool cap, bool bias) {
 size_t masked_attn_workspace_bytes(const Dims &d, int q_len) {
   const int nq = (q_len + 127) / 128;
   const int splits = splits_of(d, nq);
-  size_t n = round256(sizeof(int4) * (size_t)d.B * d.nk);
+  size_t n = round256(2 * sizeof(int4) * (size_t)d.B * d.nk);
   if (splits > 1)
     n += round256((size_t)d.BH() * nq * splits * 128 * 64 * sizeof(float)) +
          round256((size_t)d.BH() * nq * splits * 128 * sizeof(float2));
@@ -864,6 +1021,7 @@ cudaError_t launch_masked_attn(const Dims &d, const MaskedAttnLaunch &a, cudaStr
   p.out = static_cast<__nv_bfloat16 *>(a.out);
   p.lse = a.lse;
   p.dev_err = a.dev_err;
+  p.B = d.B;
   p.H = d.H;
   p.N = d.N;
   p.Nq = Nq;
@@ -874,19 +1032,28 @@ cudaError_t launch_masked_attn(const Dims &d, const MaskedAttnLaunch &a, cudaStr
   p.cap_log2 = m.softcap * kLog2e;
   p.cap_in = m.softcap > 0.f ? a.scale / m.softcap : 0.f;
   p.cap_half = 0.5f / p.cap_in;
+  // The fused cap: its coefficients must keep their range, and the bound that it takes for
+  // the row's maximum may lie 2 tanh(3/8) C above it, which costs exponents that range.
+  p.cap_a = -1.f;
+  if (p.cap_in > 1e-5f && p.cap_in < 1e5f && 0.72f * p.cap_log2 <= 64.f) {
+    p.cap_a = 0.375f / p.cap_in;
+    double k = (double)p.cap_log2 * p.cap_in;
+    for (int i = 0; i < 4; ++i, k *= (double)p.cap_in * p.cap_in) p.cap_k[i] = (float)(kTanhFit3[i] * k);
+  }
   unsigned char *ws = static_cast<unsigned char *>(a.workspace);
   int4 *blocks = reinterpret_cast<int4 *>(ws);
   p.blocks = blocks;
   const long long items = d.BH() * nq;
   if (p.splits > 1) {
-    ws += round256(sizeof(int4) * (size_t)d.B * d.nk);
+    ws += round256(2 * sizeof(int4) * (size_t)d.B * d.nk);
     p.part_o = reinterpret_cast<float *>(ws);
     ws += round256((size_t)items * p.splits * 128 * 64 * sizeof(float));
     p.part_ml = reinterpret_cast<float2 *>(ws);
   }
-  if (m.q_doc || m.q_order) {
+  if (m.q_doc || m.q_order || m.slopes) {
     const long long n = 1ll * d.B * d.nk;
-    summary_kernel<<<(unsigned)((n + 7) / 8), 256, 0, st>>>(m.k_doc, m.k_order, d.N, d.nk, d.kb, n, blocks);
+    summary_kernel<<<(unsigned)((n + 7) / 8), 256, 0, st>>>(m.k_doc, m.k_order, p.k_pos, d.N, d.nk, d.kb, n,
+                                                            blocks);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }

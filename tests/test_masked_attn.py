@@ -220,6 +220,27 @@ def test_small_large_and_saturated_scores(size, cap):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kb", [64, 128])
+@pytest.mark.parametrize("cap", [0.0, 25.0])
+@pytest.mark.parametrize("kind", ["view", "stride", "backwards", "far", "ahead", "two rates", "random"])
+def test_positions_of_every_kind(kind, cap, kb):
+    """Positions that run evenly, stand still, jump inside a tile or lie in any order, behind
+    and ahead of the queries."""
+    N = 700
+    t = torch.arange(N)
+    pos = {"view": t // 90, "stride": 3 * t, "backwards": 5000 - t, "far": t + (1 << 24) - 900, "ahead": t + 10000,
+           "two rates": torch.where(t < 330, t, 4 * t), "random": torch.randint(-2000, 2000, (N,))}[kind]
+    pos = pos.to(torch.int32).view(1, N).cuda()
+    q, k, v, g = _inputs(1, 3, N, N, seed=13)
+    qp = t.to(torch.int32).view(1, N).cuda() if kind == "ahead" else pos
+    slopes = torch.tensor([0.02, -0.01, 0.0005], device="cuda")
+    lists = _lists(1, 3, N, N, kb, 0.6, g)
+    mods = dict(slopes=slopes, q_pos=qp, k_pos=pos)
+    out, lse = _run(q, k, v, kb, lists, softcap=cap, **mods)
+    _check(q, k, v, out, lse, kb, lists, softcap=cap, **mods)
+
+
+@pytest.mark.gpu
 def test_plain_call_agrees_with_the_unmasked_kernel():
     q, k, v, g = _inputs(1, 6, 1900, 1900, seed=3)
     lists = _lists(1, 6, 1900, 1900, 128, 0.4, g)
