@@ -176,8 +176,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     masked_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
   extern __shared__ unsigned char smem_raw[];
-  unsigned char *smem = reinterpret_cast<unsigned char *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  // an offset, not a rounded pointer: the compiler still sees shared memory (32-bit addresses)
+  unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars *bar = reinterpret_cast<Bars *>(smem + kOffBar);
   uint16_t *list = reinterpret_cast<uint16_t *>(smem + kOffList);
   uint8_t *classes = smem + kOffClass;
@@ -444,7 +444,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         // positions relative to the row block's first query: exact small numbers
         int ref = 0, q_lo = 0, q_hi = 0;  // and the range of the warp's queries
         float row_pos = 0.f, slope = 0.f;
-        int4 pos[KB == 64 ? 2 : 1];  // position summaries of the next tile's blocks
         if constexpr (BIAS) {
           const int32_t *qp = p.q_pos + (long long)vb->b * p.Nq;
           ref = qp[vb->qi * 128];
@@ -466,17 +465,6 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           return u < p.N ? u : -1;
         };
-        auto load_pos = [&](int j) {
-          const volatile uint16_t *own = list + vb->skip;
-          const int4 *sum = p.blocks + (long long)(p.B + vb->b) * p.nk;
-          if constexpr (KB == 128) {
-            pos[0] = __ldg(sum + own[j]);
-          } else {
-            pos[0] = __ldg(sum + own[2 * j]);
-            if (2 * j + 1 < vb->entries) pos[1] = __ldg(sum + own[2 * j + 1]);
-            else pos[1] = pos[0];
-          }
-        };
         // the softmax warps meet (a bounded wait, as all others)
         auto meet = [&]() {
           __syncwarp();
@@ -485,7 +473,6 @@ __global__ void __launch_bounds__(kThreads, 2)
           ++meets;
           return there;
         };
-        if constexpr (BIAS) load_pos(0);
         for (int j = 0; j < vb->tiles; ++j) {
           const int J = (pass ? vb->tiles : 0) + j;
           // the warps' classes of this tile: of its block, or of its two
@@ -517,7 +504,11 @@ __global__ void __launch_bounds__(kThreads, 2)
           int side = 0;  // +1: every key at or before every query, -1: at or after, 0: mixed
           bool even = true;
           if constexpr (BIAS) {
-            const int4 p0 = pos[0], p1 = pos[KB == 64 ? 1 : 0];  // smallest, largest, first, step
+            // (summaries are 16 bytes a block: eight of them to a line of L1)
+            const volatile uint16_t *own = list + vb->skip + (KB == 128 ? j : 2 * j);
+            const int4 *sum = p.blocks + (long long)(p.B + vb->b) * p.nk;
+            const int4 p0 = __ldg(sum + own[0]);  // smallest, largest, first, step
+            const int4 p1 = KB == 64 && 2 * j + 1 < vb->entries ? __ldg(sum + own[1]) : p0;
             const int lo = min(p0.x, p1.x), hi = max(p0.y, p1.y);
             side = hi <= q_lo ? 1 : (lo >= q_hi ? -1 : 0);
             even = side != 0 && p0.w != kUneven && p1.w != kUneven;
@@ -713,8 +704,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             });
           }
           if (!ok) break;
-          if constexpr (BIAS)
-            if (j + 1 < tiles) load_pos(j + 1);
           if (j > 0) {
             ok = warp_wait(&bar->o_done, (J - 1) & 1, abort);
             if (!ok) break;
