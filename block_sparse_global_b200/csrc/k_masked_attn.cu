@@ -94,11 +94,6 @@ RESS_DEV float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// A wait of a whole warp: every lane sees the same answer, so that a warp that gives up
-// leaves its loop together.
-RESS_DEV bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
-}
 RESS_DEV void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 RESS_DEV uint64_t fmul2(uint64_t a, uint64_t b) {
@@ -465,13 +460,19 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           return u < p.N ? u : -1;
         };
-        // the softmax warps meet (a bounded wait, as all others)
-        auto meet = [&]() {
+        // A wait that gives up does not leave the tile: the lanes stay together, later waits
+        // return at once (abort), and the loop ends after a vote.
+        auto wait = [&](uint64_t *which, uint32_t parity) {
+          if (!mbar_wait(which, parity, abort)) {
+            ok = false;
+            *abort = 1;
+          }
+        };
+        auto meet = [&]() {  // the softmax warps meet
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar->meet);
-          const bool there = warp_wait(&bar->meet, meets & 1, abort);
+          wait(&bar->meet, meets & 1);
           ++meets;
-          return there;
         };
         for (int j = 0; j < vb->tiles; ++j) {
           const int J = (pass ? vb->tiles : 0) + j;
@@ -486,16 +487,14 @@ __global__ void __launch_bounds__(kThreads, 2)
           cls &= (1u << (2 * vb->active)) - 1;
           const uint32_t code = (cls >> (2 * warp)) & 3;
           if (cls & ~(cls >> 1) & 0x55u) {  // mixed for some warp
-            ok = meet();  // the last mixed tile's arrays have been read
-            if (!ok) break;
+            meet();  // the last mixed tile's arrays have been read
             for (int c = tid; c < 128; c += 32 * vb->active) {
               const int u = key_of(j, c);
               const long long at = (long long)vb->b * p.N + u;
               m_doc[c] = u < 0 ? -1 : (p.k_doc ? max(__ldg(p.k_doc + at), -1) : 0);
               m_order[c] = u < 0 || !p.k_order ? 0 : __ldg(p.k_order + at);
             }
-            ok = meet();
-            if (!ok) break;
+            meet();
           }
           // The bias of column c of half i, where the keys lie on one side of the warp's
           // queries: shift[i] + step[i] (c mod 64) if positions run evenly in each half (the
@@ -528,8 +527,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               __syncwarp();
             }
           }
-          ok = warp_wait(&bar->s_full, J & 1, abort);
-          if (!ok) break;
+          wait(&bar->s_full, J & 1);
           tc_fence_after();
           uint32_t sv[128];
 #pragma unroll
@@ -554,8 +552,8 @@ __global__ void __launch_bounds__(kThreads, 2)
               pk[c] = pack_bf16x2(f2lo(e), f2hi(e));
               if (c == 31) {
                 // keys 0..63 of P: free once the first half of the previous product is done
-                if (j > 0) ok = warp_wait(&bar->o_half, (J - 1) & 1, abort);
-                if (ok) tmem_st32(trow + kColP, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+                if (j > 0) wait(&bar->o_half, (J - 1) & 1);
+                tmem_st32(trow + kColP, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
               }
             }
             const uint64_t a = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
@@ -582,8 +580,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (code == kNone) {
 #pragma unroll
             for (int c = 0; c < 64; ++c) pk[c] = 0u;
-            if (j > 0) ok = warp_wait(&bar->o_half, (J - 1) & 1, abort);
-            if (ok) tmem_st32(trow + kColP, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+            if (j > 0) wait(&bar->o_half, (J - 1) & 1);
+            tmem_st32(trow + kColP, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
           } else if (CAP && !BIAS && fused) {
             // the cap inside the exponent, s P(s^2) with the scales in its coefficients; the
             // cap of the largest |s| bounds the row's scores
@@ -703,10 +701,8 @@ __global__ void __launch_bounds__(kThreads, 2)
               return ffma2(s2, sc2, c < 32 ? n0 : n1);
             });
           }
-          if (!ok) break;
           if (j > 0) {
-            ok = warp_wait(&bar->o_done, (J - 1) & 1, abort);
-            if (!ok) break;
+            wait(&bar->o_done, (J - 1) & 1);
             tc_fence_after();
             if (__any_sync(0xffffffffu, rescale)) {
               uint32_t ov[32];
@@ -726,8 +722,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             // which rows of V hold a value that is not finite
             const int sp = J % kVStages;
             unsigned char *vt = smem + kOffV + sp * kTile;
-            ok = warp_wait(&bar->v_full[sp], (J / kVStages) & 1, abort);
-            if (!ok) break;
+            wait(&bar->v_full[sp], (J / kVStages) & 1);
             for (int r = warp; r < 4; r += vb->active) {
               const uint32_t *vr = reinterpret_cast<const uint32_t *>(vt + (32 * r + lane) * 128);
               bool inf = false;
@@ -739,8 +734,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               const uint32_t bits = __ballot_sync(0xffffffffu, inf);
               if (lane == 0) *reinterpret_cast<volatile uint32_t *>(&bar->vflag[r]) = bits;
             }
-            ok = meet();
-            if (!ok) break;
+            meet();
             const volatile uint32_t *vbad = bar->vflag;
             if ((vbad[0] | vbad[1] | vbad[2] | vbad[3]) != 0) {
               // they go to the rows that see them, and out of the tile
@@ -778,8 +772,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
               tmem_wait_st();
               if (j == 0 && lane == 0) *reinterpret_cast<volatile int *>(&bar->o_init) = 1;
-              ok = meet();
-              if (!ok) break;
+              meet();
               for (int r = warp; r < 4; r += vb->active) {
                 uint16_t *vr = reinterpret_cast<uint16_t *>(vt + (32 * r + lane) * 128);
 #pragma unroll 1
@@ -788,16 +781,18 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
               fence_async_shared();
             }
-            ok = meet();  // the flags have been read
-            if (!ok) break;
+            meet();  // the flags have been read
           }
           tc_fence_before();
           __syncwarp();
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           if (lane == 0) mbar_arrive(&bar->p_full);
         }
         const int t = vb->qi * 128 + tid;
         const long long slot = ((long long)vb->bh * p.nq + vb->qi) * p.splits + blockIdx.y;
-        if (ok) ok = warp_wait(&bar->o_done, ((pass + 1) * vb->tiles - 1) & 1, abort);
+        if (ok) wait(&bar->o_done, ((pass + 1) * vb->tiles - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
           report_error(p.dev_err, RESS_ERR_DEVICE_TIMEOUT);
           *abort = 1;
@@ -941,6 +936,39 @@ __global__ void __launch_bounds__(256) summary_kernel(const int32_t *__restrict_
   }
 }
 
+// Rows of a masked call, one warp each: how many of the row's kept blocks some query sees, for
+// a launch order of the longest rows first.
+__global__ void __launch_bounds__(256) plan_kernel(const __grid_constant__ Params p, long long rows,
+                                                   int32_t *__restrict__ count) {
+  const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (item >= rows) return;
+  const long long bh = item / p.nq;
+  const int qi = (int)(item - bh * p.nq), b = (int)(bh / p.H);
+  int dmin = INT_MAX, dmax = INT_MIN, omax = INT_MIN;
+  for (int t = qi * 128 + lane; t < min(p.Nq, qi * 128 + 128); t += 32) {
+    const int d = p.q_doc ? p.q_doc[(long long)b * p.Nq + t] : 0;
+    if (d < 0) continue;
+    dmin = min(dmin, d);
+    dmax = max(dmax, d);
+    if (p.q_order) omax = max(omax, p.q_order[(long long)b * p.Nq + t]);
+  }
+  dmin = __reduce_min_sync(0xffffffffu, dmin);
+  dmax = __reduce_max_sync(0xffffffffu, dmax);
+  omax = __reduce_max_sync(0xffffffffu, omax);
+  const int cnt = p.kv_cnt ? min(p.kv_cnt[item], p.nk) : p.nk;
+  int n = 0;
+  for (int j = lane; j < cnt; j += 32) {
+    const int kb = p.kv_idx ? p.kv_idx[item * p.nk + j] : j;
+    if (kb < 0 || kb >= p.nk) continue;
+    const int4 s = p.blocks[(long long)b * p.nk + kb];
+    const bool doc = !p.q_doc || (dmax >= 0 && s.y >= 0 && max(s.x, 0) <= dmax && s.y >= dmin);
+    n += doc && (!p.q_order || s.z <= omax);
+  }
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0) count[item] = n;
+}
+
 // Rows of a problem without keys: zero, and lse = -inf.
 __global__ void __launch_bounds__(256) no_keys_kernel(long long rows, uint4 *__restrict__ out,
                                                       float *__restrict__ lse) {
@@ -951,13 +979,23 @@ __global__ void __launch_bounds__(256) no_keys_kernel(long long rows, uint4 *__r
 }
 
 // CTAs that share a row: as many as keep the whole card (two per SM) busy, each with some
-// tiles of the longest possible row.
+// tiles of the longest possible row; long rows are split on into up to four times as many,
+// since kept lists and masks make them uneven (a part's sums cost 32 KB each way).
 constexpr int kSlots = 2 * 148, kTilesPerSplit = 4;
 int splits_of(const Dims &d, int nq) {
   const long long items = d.BH() * nq;
   const int tiles = (int)((d.N + 127) / 128);
-  if (items == 0 || items * 2 > kSlots) return 1;
-  return (int)std::max(1ll, std::min((long long)(kSlots / items), (long long)(tiles / kTilesPerSplit)));
+  if (items == 0) return 1;
+  long long n = std::max(1ll, std::min(kSlots / items, (long long)(tiles / kTilesPerSplit)));
+  while (items * n * 2 <= 4 * kSlots && tiles >= 2 * n * 4 * kTilesPerSplit) n *= 2;
+  return (int)n;
+}
+
+// Masked rows are put in order, longest first, where they come in more than one wave and
+// are long enough for the tail to matter (two small kernels, about 10 us).
+bool plans_order(const Dims &d, int nq) {
+  const long long items = d.BH() * nq;
+  return items > kSlots && items * ((d.N + 127) / 128) >= 64 * kSlots;
 }
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -974,7 +1012,8 @@ KernelFn pick(bool cap, bool bias) {
 size_t masked_attn_workspace_bytes(const Dims &d, int q_len) {
   const int nq = (q_len + 127) / 128;
   const int splits = splits_of(d, nq);
-  size_t n = round256(2 * sizeof(int4) * (size_t)d.B * d.nk);
+  size_t n = plans_order(d, nq) ? 2 * round256(sizeof(int32_t) * (size_t)d.BH() * nq) : 0;
+  n += round256(2 * sizeof(int4) * (size_t)d.B * d.nk);
   if (splits > 1)
     n += round256((size_t)d.BH() * nq * splits * 128 * 64 * sizeof(float)) +
          round256((size_t)d.BH() * nq * splits * 128 * sizeof(float2));
@@ -1033,8 +1072,14 @@ cudaError_t launch_masked_attn(const Dims &d, const MaskedAttnLaunch &a, cudaStr
   int4 *blocks = reinterpret_cast<int4 *>(ws);
   p.blocks = blocks;
   const long long items = d.BH() * nq;
+  ws += round256(2 * sizeof(int4) * (size_t)d.B * d.nk);
+  int32_t *count = nullptr, *sorted = nullptr;
+  if (plans_order(d, nq)) {
+    count = reinterpret_cast<int32_t *>(ws);
+    sorted = reinterpret_cast<int32_t *>(ws + round256(sizeof(int32_t) * (size_t)items));
+    ws += 2 * round256(sizeof(int32_t) * (size_t)items);
+  }
   if (p.splits > 1) {
-    ws += round256(2 * sizeof(int4) * (size_t)d.B * d.nk);
     p.part_o = reinterpret_cast<float *>(ws);
     ws += round256((size_t)items * p.splits * 128 * 64 * sizeof(float));
     p.part_ml = reinterpret_cast<float2 *>(ws);
@@ -1045,6 +1090,16 @@ cudaError_t launch_masked_attn(const Dims &d, const MaskedAttnLaunch &a, cudaStr
                                                             blocks);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+  }
+  if (sorted && !p.order && (m.q_doc || m.q_order)) {
+    plan_kernel<<<(unsigned)((items + 7) / 8), 256, 0, st>>>(p, items, count);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    Dims rows = d;
+    rows.nb = rows.nq = nq;
+    e = launch_schedule(rows, count, sorted, st);
+    if (e != cudaSuccess) return e;
+    p.order = sorted;
   }
   KernelFn kern = d.kb == 64 ? pick<64>(m.softcap > 0.f, m.slopes != nullptr)
                              : pick<128>(m.softcap > 0.f, m.slopes != nullptr);

@@ -211,6 +211,22 @@ def test_against_64_bits(Bn, H, N, Nq, kb, keep, cap, docs, pad, order, bias, sh
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Bn,H,N,Nq,kb,keep,cap,docs,pad,order,bias", [
+    (1, 16, 8000, 8000, 128, 0.5, 0.0, 3, 150, "none", 0.0), (2, 6, 7777, 7777, 64, 0.5, 30.0, 2, 33, "token", 0.01),
+    (1, 16, 9000, 1500, 128, 0.5, 0.0, 2, 100, "token", 0.0), (1, 16, 9001, 1374, 64, 0.25, 0.0, 0, 0, "view", 0.02)])
+def test_many_rows_and_long_rows(Bn, H, N, Nq, kb, keep, cap, docs, pad, order, bias):
+    """Rows enough to be put in order by what they see, and rows long enough for several parts."""
+    torch.manual_seed(N)
+    q, k, v, g = _inputs(Bn, H, N, Nq, seed=N)
+    lists = _lists(Bn, H, Nq, N, kb, keep, g)
+    mods = _arrays(Bn, N, Nq, docs, pad, order, bias, H, g)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = _run(q, k, v, kb, lists, dev_err=err, softcap=cap, **mods)
+    assert int(err) == 0
+    _check(q, k, v, out, lse, kb, lists, softcap=cap, **mods)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("size", [0.05, 6.0, 40.0])
 @pytest.mark.parametrize("cap", [0.0, 5.0, 50.0])
 def test_small_large_and_saturated_scores(size, cap):
