@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 // ------------------------------------------------------------------------ join
 // One warp per query row: out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.  A split with
 // l = 0 saw no key (its O is not written); one with l < 0 met an error and leaves the row
-// as it was.
+// as it was.  A lane weighs a split, so that the O's loads depend on nothing but the weights.
 __global__ void __launch_bounds__(256) join_kernel(const float *__restrict__ part_o,
                                                    const float2 *__restrict__ part_ml, int splits, int nq,
                                                    int Nq, long long rows, __nv_bfloat16 *__restrict__ out,
@@ -875,15 +875,28 @@ __global__ void __launch_bounds__(256) join_kernel(const float *__restrict__ par
   if (__any_sync(0xffffffffu, bad)) return;
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float l = 0.f, o0 = 0.f, o1 = 0.f;
-  for (int s = 0; s < splits; ++s) {
-    const float2 ml = part_ml[(slot0 + s) * 128 + r];
-    if (ml.y == 0.f) continue;
-    const float w = ex2_approx(ml.x - m);
-    const float2 v = *reinterpret_cast<const float2 *>(part_o + ((slot0 + s) * 128 + r) * 64 + 2 * lane);
-    l += w * ml.y;
-    o0 += w * v.x;
-    o1 += w * v.y;
+  for (int s0 = 0; s0 < splits; s0 += 32) {
+    const int n = min(32, splits - s0);
+    float w = 0.f;
+    bool some = false;
+    if (lane < n) {
+      const float2 ml = part_ml[(slot0 + s0 + lane) * 128 + r];
+      some = ml.y != 0.f;
+      w = some ? ex2_approx(ml.x - m) : 0.f;
+      l += w * ml.y;
+    }
+    const uint32_t mask = __ballot_sync(0xffffffffu, some);
+    const float *src = part_o + ((slot0 + s0) * 128 + r) * 64 + 2 * lane;
+#pragma unroll 8
+    for (int s = 0; s < n; ++s) {
+      const float ws = __shfl_sync(0xffffffffu, w, s);
+      float2 v = make_float2(0.f, 0.f);
+      if (mask >> s & 1) v = *reinterpret_cast<const float2 *>(src + (long long)s * 128 * 64);
+      o0 += ws * v.x;
+      o1 += ws * v.y;
+    }
   }
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   const bool none = l == 0.f;
   const float inv = 1.0f / l;
   reinterpret_cast<uint32_t *>(out + row * 64)[lane] = none ? 0u : pack_bf16x2(o0 * inv, o1 * inv);

@@ -376,11 +376,15 @@ def _launch(name: str, device, stream, *args):
     stream."""
     if device.type != "cuda":
         raise ValueError(f"{name} takes CUDA tensors, got {device}")
+    if stream is None:  # (the same stream as torch.cuda.current_stream, without its lookups)
+        stream = torch._C._cuda_getCurrentRawStream(device.index)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
-            st = getattr(load(), name)(*args, _stream(stream))
+            st = getattr(load(), name)(*args, int(stream))
     else:
-        st = getattr(load(), name)(*args, _stream(stream))
+        st = getattr(_lib or load(), name)(*args, int(stream))
     _check(name, st)
 
 
