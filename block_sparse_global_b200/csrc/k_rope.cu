@@ -16,9 +16,9 @@
 // quarter turn is taken off as an integer too, so that only an angle of at most pi / 4 is
 // rounded to fp32 (an error of 2^-25 relative, against 2^-24 pi for a whole turn).
 //
-// What bounds it: HBM.  Every element is read and written once.  A warp takes one token:
-// its angles are the same for every head, so they are computed once per token, by lanes
-// in parallel, and stay in registers while the warp walks the token's heads.
+// What bounds it: HBM.  Every element is read and written once.  The angles of a token are
+// the same for every head, so a CTA takes some tokens with all their heads, computes their
+// angles once into shared memory, and its warps then walk (heads, token) pieces.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -72,8 +72,9 @@ struct TokenParams {
   const int32_t *positions;  // [B or 1][N][axes], or null: the token's index
   long long pos_b;
   int views, specials, view_tokens;  // view_tokens = 0: rows keep their places
-  int groups;                        // warps that share a token's heads
-  long long tasks;                   // B * N * groups
+  int groups;                        // element form: warps that share a token's heads
+  long long tasks;                   // element form: B * N * groups
+  int tile, tiles;                   // 16-byte form: tokens of a CTA, CTAs of a batch entry
   uint64_t phase[kMaxPairs];         // turns per position of each pair of a section
 };
 
@@ -85,29 +86,34 @@ RESS_DEV int target_row(const TokenParams &p, int t) {
   return r >= p.specials ? v * patch + r - p.specials : p.views * patch + v * p.specials + r;
 }
 
-// (amplitude cos, amplitude sin) of every pair of a token, in section order.
+// (amplitude cos, amplitude sin) of pair i of a token, in section order.
+RESS_DEV float2 pair_angle(const TokenParams &p, uint64_t phase, int b, int t, int axis) {
+  const long long pos =
+      p.positions ? (long long)__ldg(p.positions + b * p.pos_b + (long long)t * p.axes + axis) : t;
+  const uint64_t turn = (uint64_t)pos * phase;
+  const uint32_t quarter = (uint32_t)((turn + (1ull << 61)) >> 62);
+  const long long rest = (long long)(turn - ((uint64_t)quarter << 62));
+  float s, c;
+  sincospif(__ll2float_rn(rest) * 0x1p-63f, &s, &c);
+  if (quarter & 1) {
+    const float x = s;
+    s = c;
+    c = -x;
+  }
+  if (quarter & 2) {
+    s = -s;
+    c = -c;
+  }
+  return make_float2(p.amplitude * c, p.sign * p.amplitude * s);
+}
+
+// The angles of a token, by the lanes of a warp.
 RESS_DEV void token_angles(const TokenParams &p, const uint64_t *phase, int b, int t, int lane,
                            float2 *cs) {
   const int pairs = p.rot >> 1, per = pairs / p.axes;
   for (int i = lane; i < pairs; i += 32) {
     const int a = i / per;
-    const long long pos =
-        p.positions ? (long long)__ldg(p.positions + b * p.pos_b + (long long)t * p.axes + a) : t;
-    const uint64_t turn = (uint64_t)pos * phase[i - a * per];
-    const uint32_t quarter = (uint32_t)((turn + (1ull << 61)) >> 62);
-    const long long rest = (long long)(turn - ((uint64_t)quarter << 62));
-    float s, c;
-    sincospif(__ll2float_rn(rest) * 0x1p-63f, &s, &c);
-    if (quarter & 1) {
-      const float t = s;
-      s = c;
-      c = -t;
-    }
-    if (quarter & 2) {
-      s = -s;
-      c = -c;
-    }
-    cs[i] = make_float2(p.amplitude * c, p.sign * p.amplitude * s);
+    cs[i] = pair_angle(p, phase[i - a * per], b, t, a);
   }
 }
 
@@ -117,138 +123,216 @@ RESS_DEV float row_sum(float v, int lanes) {
 }
 
 // ------------------------------------------------------------------- 16-byte form
-// A row is D * sizeof(T) / 16 lanes (a power of two up to 32), one 16-byte chunk each, so a
-// warp holds several heads of a token at a time; a lane keeps the same chunk of the row for
-// every head, and with it the same angles.  Pairs of the interleaved layout lie inside a
-// chunk; pairs of the half layout lie in chunks half a section apart and meet by shuffle.
+// A lane holds two 16-byte chunks of a row, so that a rotated pair never leaves the lane:
+// chunks half a section apart in the half layout, neighbours in the interleaved one.  A row
+// takes D / 2V lanes, rounded up to a power of two (the rest idle), and a warp's pass several
+// heads of one token.  The passes of all tensors and the CTA's tokens form one list, pass by
+// pass, of which each warp takes an equal stretch, with the loads of the next pieces in
+// flight; weights and biases stay in registers until the tensor changes.
+// Both sums of the layer norm are over centred values, in fp32.
+constexpr int kAngleFloats = 4096;  // (cos, sin) of the CTA's tokens: 16 KB
+constexpr int kPieces = 4;          // pieces in flight per warp
+
+RESS_DEV uint64_t pk2(float lo, float hi) {
+  return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
+}
+RESS_DEV float lo2(uint64_t v) { return __uint_as_float((uint32_t)v); }
+RESS_DEV float hi2(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+RESS_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+RESS_DEV uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+RESS_DEV uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// 16 bytes as pairs of fp32, and back with one rounding.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) token_vec_kernel(const __grid_constant__ TokenParams p) {
-  constexpr int V = 16 / sizeof(T);
-  constexpr int U = 4;  // loads in flight per lane
-  __shared__ uint64_t phase[kMaxPairs];
-  __shared__ __align__(16) float wb[4][kMaxDim];
-  __shared__ float2 cs_all[kWarps][kMaxPairs];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int pairs = p.rot >> 1;
-  if (pairs > 0)
-    for (int i = tid; i < pairs / p.axes; i += kThreads) phase[i] = p.phase[i];
-  for (int i = tid; i < p.D; i += kThreads) {
+RESS_DEV void unpack(const uint4 &raw, uint64_t *x);
+template <>
+RESS_DEV void unpack<float>(const uint4 &raw, uint64_t *x) {
+  x[0] = ((uint64_t)raw.y << 32) | raw.x;
+  x[1] = ((uint64_t)raw.w << 32) | raw.z;
+}
+template <>
+RESS_DEV void unpack<__nv_bfloat16>(const uint4 &raw, uint64_t *x) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      wb[2 * a][i] = p.part[a].weight ? p.part[a].weight[i] : 1.f;
-      wb[2 * a + 1][i] = p.part[a].bias ? p.part[a].bias[i] : 0.f;
+  for (int i = 0; i < 4; ++i) x[i] = ((uint64_t)(w[i] & 0xffff0000u) << 32) | (w[i] << 16);
+}
+template <>
+RESS_DEV void unpack<__half>(const uint4 &raw, uint64_t *x) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+    x[i] = pk2(v.x, v.y);
+  }
+}
+template <typename T>
+RESS_DEV uint4 repack(const uint64_t *x);
+template <>
+RESS_DEV uint4 repack<float>(const uint64_t *x) {
+  return make_uint4((uint32_t)x[0], (uint32_t)(x[0] >> 32), (uint32_t)x[1], (uint32_t)(x[1] >> 32));
+}
+template <>
+RESS_DEV uint4 repack<__nv_bfloat16>(const uint64_t *x) {
+  return make_uint4(pack_bf16x2(lo2(x[0]), hi2(x[0])), pack_bf16x2(lo2(x[1]), hi2(x[1])),
+                    pack_bf16x2(lo2(x[2]), hi2(x[2])), pack_bf16x2(lo2(x[3]), hi2(x[3])));
+}
+template <>
+RESS_DEV uint4 repack<__half>(const uint64_t *x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(lo2(x[i]), hi2(x[i]));
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// HALF: the pair layout; NORM: ress_norm.
+template <typename T, bool HALF, int NORM>
+__global__ void __launch_bounds__(kThreads) token_vec_kernel(const __grid_constant__ TokenParams p) {
+  constexpr int V = 16 / sizeof(T);  // elements of a chunk
+  __shared__ __align__(16) float cs[kAngleFloats];
+  __shared__ __align__(16) float wb[4][kMaxDim];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.x / p.tiles, t0 = (blockIdx.x - b * p.tiles) * p.tile;
+  const int nt = min(p.tile, p.N - t0);
+  const int pairs = p.rot >> 1, slots = p.D >> 1;  // cos, then sin, of `slots` pairs a token
+  if (pairs > 0) {
+    const int per = pairs / p.axes;
+    for (int i = tid; i < nt * pairs; i += kThreads) {
+      const int t = i / pairs, k = i - t * pairs, a = k / per;
+      const float2 v = pair_angle(p, p.phase[k - a * per], b, t0 + t, a);
+      cs[2 * slots * t + k] = v.x;
+      cs[2 * slots * t + slots + k] = v.y;
+    }
+  }
+  if (NORM != RESS_NORM_NONE) {
+    for (int i = tid; i < p.D; i += kThreads) {
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        wb[2 * a][i] = p.part[a].weight ? p.part[a].weight[i] : 1.f;
+        wb[2 * a + 1][i] = p.part[a].bias ? p.part[a].bias[i] : 0.f;
+      }
     }
   }
   __syncthreads();
-  const int lpr = p.D / V, rpw = 32 / lpr;  // lanes per row, rows per warp
-  const int sub = lane / lpr, chunk = lane - sub * lpr;
-  float2 *cs = cs_all[warp];
-  // iterations of each part: rpw heads at a time
+  const int used = p.D / (2 * V);  // lanes of a row that hold something
+  int lpr = 1;
+  while (lpr < used) lpr <<= 1;
+  const int rpw = 32 / lpr, sub = lane / lpr, own = lane & (lpr - 1);
+  const bool holds = own < used;
+  // this lane's chunks: a is element ca of the row, b element cb
+  int ca = 2 * own * V, cb = ca + V;
+  bool turned = pairs > 0 && own * V < pairs;  // (interleaved: up to pair `pairs`)
+  if (HALF && turned) {
+    const int hl = p.rot / p.axes / (2 * V);  // chunks of half a section
+    const int sec = own / hl;
+    ca = (sec * 2 * hl + own - sec * hl) * V;
+    cb = ca + hl * V;
+  }
   const int it1 = (p.part[0].heads + rpw - 1) / rpw;
   const int it2 = it1 + (p.parts > 1 ? (p.part[1].heads + rpw - 1) / rpw : 0);
   const int its = it2 + (p.parts > 2 ? (p.part[2].heads + rpw - 1) / rpw : 0);
-  // this lane's pairs: shuffle partner and first pair (half layout)
-  const bool half = p.layout == RESS_ROPE_HALF;
-  int partner = lane, pair0 = chunk * V / 2;
-  bool second = false, turned = chunk * V < p.rot;
-  if (half && turned) {
-    const int hl = p.rot / p.axes / (2 * V);  // chunks in half a section
-    const int sec = chunk / (2 * hl), at = chunk - sec * 2 * hl;
-    second = at >= hl;
-    partner = second ? lane - hl : lane + hl;
-    pair0 = (sec * hl + (second ? at - hl : at)) * V;
-  }
-  const long long stride = (long long)gridDim.x * kWarps;
-  for (long long task = (long long)blockIdx.x * kWarps + warp; task < p.tasks; task += stride) {
-    const long long token = task / p.groups;
-    const int group = (int)(task - token * p.groups);
-    const int b = (int)(token / p.N), t = (int)(token - (long long)b * p.N);
-    const int t_out = target_row(p, t);
-    float c[V], s[V];
-    if (pairs > 0) {
-      __syncwarp();
-      token_angles(p, phase, b, t, lane, cs);
-      __syncwarp();
+  const int i0 = its * nt * warp / kWarps, i1 = its * nt * (warp + 1) / kWarps;
+  int cur = -1;              // tensor of the weights in registers
+  uint64_t w[V], bias[V];    // V / 2 pairs of chunk a, then of chunk b
+  for (int i = i0; i < i1; i += kPieces) {
+    uint4 raw[kPieces][2];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const int at = half ? pair0 + e : pair0 + (e >> 1);
-        const float2 v = turned && at < pairs ? cs[at] : make_float2(1.f, 0.f);
-        c[e] = v.x;
-        s[e] = v.y;
+    for (int u = 0; u < kPieces; ++u) {
+      const int pass = (i + u) / nt, t = i + u - pass * nt;
+      const int which = pass < it1 ? 0 : (pass < it2 ? 1 : 2);
+      const Part &q = p.part[which];
+      const int h = (pass - (which == 0 ? 0 : (which == 1 ? it1 : it2))) * rpw + sub;
+      raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+      if (i + u < i1 && holds && h < q.heads) {
+        const T *src = static_cast<const T *>(q.in) + b * q.in_b + h * q.in_h + (t0 + t) * q.in_t;
+        raw[u][0] = *reinterpret_cast<const uint4 *>(src + ca);
+        raw[u][1] = *reinterpret_cast<const uint4 *>(src + cb);
       }
     }
-    const int i0 = (int)((long long)its * group / p.groups);
-    const int i1 = (int)((long long)its * (group + 1) / p.groups);
-    for (int i = i0; i < i1; i += U) {
-      uint4 raw[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = i + u;
-        if (k < i1) {
-          const int which = k < it1 ? 0 : (k < it2 ? 1 : 2);
-          const Part &q = p.part[which];
-          const int h = (k - (which == 0 ? 0 : (which == 1 ? it1 : it2))) * rpw + sub;
-          raw[u] = make_uint4(0, 0, 0, 0);
-          if (h < q.heads)
-            raw[u] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(q.in) + b * q.in_b +
-                                                      h * q.in_h + t * q.in_t + chunk * V);
+    for (int u = 0; u < kPieces; ++u) {
+      if (i + u >= i1) break;
+      const int pass = (i + u) / nt, t = i + u - pass * nt;
+      const int which = pass < it1 ? 0 : (pass < it2 ? 1 : 2);
+      const Part &q = p.part[which];
+      const int h = (pass - (which == 0 ? 0 : (which == 1 ? it1 : it2))) * rpw + sub;
+      if (q.work) {
+        uint64_t x[V];
+        unpack<T>(raw[u][0], x);
+        unpack<T>(raw[u][1], x + V / 2);
+        if (NORM != RESS_NORM_NONE) {
+          if (which != cur) {
+            cur = which;
+            const int ra = holds ? ca : 0, rb = holds ? cb : 0;
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) {
+              w[e] = *reinterpret_cast<const uint64_t *>(&wb[2 * which][ra + 2 * e]);
+              w[V / 2 + e] = *reinterpret_cast<const uint64_t *>(&wb[2 * which][rb + 2 * e]);
+              bias[e] = *reinterpret_cast<const uint64_t *>(&wb[2 * which + 1][ra + 2 * e]);
+              bias[V / 2 + e] = *reinterpret_cast<const uint64_t *>(&wb[2 * which + 1][rb + 2 * e]);
+            }
+          }
+          if (NORM == RESS_NORM_LAYER) {
+            uint64_t m = x[0];
+#pragma unroll
+            for (int e = 1; e < V; ++e) m = add2(m, x[e]);
+            const float total = row_sum(lo2(m) + hi2(m), lpr);
+            const float mean = holds ? total / p.D : 0.f;  // idle lanes stay 0
+            const uint64_t m2 = pk2(-mean, -mean);
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[e] = add2(x[e], m2);
+          }
+          uint64_t ss = mul2(x[0], x[0]);
+#pragma unroll
+          for (int e = 1; e < V; ++e) ss = fma2(x[e], x[e], ss);
+          const float r = rsqrtf(row_sum(lo2(ss) + hi2(ss), lpr) / p.D + p.eps);
+          const uint64_t r2 = pk2(r, r);
+#pragma unroll
+          for (int e = 0; e < V; ++e) x[e] = fma2(mul2(x[e], r2), w[e], bias[e]);
         }
+        if (turned) {
+          const uint64_t *c = reinterpret_cast<const uint64_t *>(cs + 2 * slots * t + own * V);
+          const uint64_t *s = c + slots / 2;
+#pragma unroll
+          for (int e = 0; e < V / 2; ++e) {
+            const uint64_t ce = c[e], se = s[e];
+            if (HALF) {  // pairs (x_a, x_b)
+              const uint64_t ns = se ^ 0x8000000080000000ull;
+              const uint64_t a = x[e], d = x[V / 2 + e];
+              x[e] = fma2(d, ns, mul2(a, ce));
+              x[V / 2 + e] = fma2(a, se, mul2(d, ce));
+            } else {  // pairs inside the packed values
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                if (own * V + 2 * e + k >= pairs) continue;
+                const float cc = k ? hi2(ce) : lo2(ce), sn = k ? hi2(se) : lo2(se);
+                const float a = lo2(x[2 * e + k]), d = hi2(x[2 * e + k]);
+                x[2 * e + k] = pk2(fmaf(-d, sn, a * cc), fmaf(a, sn, d * cc));
+              }
+            }
+          }
+        }
+        raw[u][0] = repack<T>(x);
+        raw[u][1] = repack<T>(x + V / 2);
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = i + u;
-        if (k >= i1) break;
-        const int which = k < it1 ? 0 : (k < it2 ? 1 : 2);
-        const Part &q = p.part[which];
-        const int h = (k - (which == 0 ? 0 : (which == 1 ? it1 : it2))) * rpw + sub;
-        if (q.work) {
-          T *e_ = reinterpret_cast<T *>(&raw[u]);
-          float x[V];
-#pragma unroll
-          for (int e = 0; e < V; ++e) x[e] = to_f32<T>(e_[e]);
-          if (p.norm != RESS_NORM_NONE) {
-            float mean = 0.f;
-            if (p.norm == RESS_NORM_LAYER) {
-              float m = 0.f;
-#pragma unroll
-              for (int e = 0; e < V; ++e) m += x[e];
-              mean = row_sum(m, lpr) / p.D;
-            }
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              x[e] -= mean;
-              ss += x[e] * x[e];
-            }
-            const float r = rsqrtf(row_sum(ss, lpr) / p.D + p.eps);
-            const float *w = wb[2 * which] + chunk * V, *bb = wb[2 * which + 1] + chunk * V;
-#pragma unroll
-            for (int e = 0; e < V; ++e) x[e] = x[e] * r * w[e] + bb[e];
-          }
-          if (pairs > 0) {
-            if (half) {
-#pragma unroll
-              for (int e = 0; e < V; ++e) {
-                const float y = __shfl_sync(0xffffffffu, x[e], partner);
-                if (turned) x[e] = second ? x[e] * c[e] + y * s[e] : x[e] * c[e] - y * s[e];
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < V; e += 2) {
-                if (chunk * V + e < p.rot) {
-                  const float a = x[e], d = x[e + 1];
-                  x[e] = a * c[e] - d * s[e];
-                  x[e + 1] = d * c[e] + a * s[e];
-                }
-              }
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < V; ++e) e_[e] = from_f32<T>(x[e]);
-        }
-        if (h < q.heads)
-          *reinterpret_cast<uint4 *>(static_cast<T *>(q.out) + b * q.out_b + h * q.out_h +
-                                     t_out * q.out_t + chunk * V) = raw[u];
+      if (holds && h < q.heads) {
+        T *dst = static_cast<T *>(q.out) + b * q.out_b + h * q.out_h + target_row(p, t0 + t) * q.out_t;
+        *reinterpret_cast<uint4 *>(dst + ca) = raw[u][0];
+        *reinterpret_cast<uint4 *>(dst + cb) = raw[u][1];
       }
     }
   }
@@ -355,26 +439,46 @@ __global__ void __launch_bounds__(kThreads) token_elem_kernel(const __grid_const
 
 bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
+template <typename T, bool HALF>
+void launch_vec(const TokenParams &p, unsigned ctas, cudaStream_t st) {
+  if (p.norm == RESS_NORM_NONE)
+    token_vec_kernel<T, HALF, RESS_NORM_NONE><<<ctas, kThreads, 0, st>>>(p);
+  else if (p.norm == RESS_NORM_RMS)
+    token_vec_kernel<T, HALF, RESS_NORM_RMS><<<ctas, kThreads, 0, st>>>(p);
+  else
+    token_vec_kernel<T, HALF, RESS_NORM_LAYER><<<ctas, kThreads, 0, st>>>(p);
+}
+
 template <typename T>
 cudaError_t launch_typed(TokenParams &p, int sms, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(T);
-  // the 16-byte form: chunks fill a power-of-two share of a warp, every row starts on a
-  // 16-byte boundary, and the pairs of the half layout lie whole chunks apart
-  const int lpr = p.D / V;
-  bool vec = p.D % V == 0 && lpr <= 32 && (lpr & (lpr - 1)) == 0;
-  if (p.rot > 0 && p.layout == RESS_ROPE_HALF) vec = vec && (p.rot / p.axes) % (2 * V) == 0;
+  // the 16-byte form: rows are whole pairs of chunks on 16-byte boundaries, and the pairs of
+  // the half layout lie whole chunks apart
+  const bool half = p.layout == RESS_ROPE_HALF;
+  bool vec = p.D % (2 * V) == 0;
+  if (p.rot > 0 && half) vec = vec && (p.rot / p.axes) % (2 * V) == 0;
   int rows = 0;
   for (int i = 0; i < p.parts; ++i) {
     const Part &q = p.part[i];
     vec = vec && aligned(q.in, 16) && aligned(q.out, 16);
     for (long long s : {q.in_b, q.in_h, q.in_t, q.out_b, q.out_h, q.out_t}) vec = vec && s % V == 0;
-    rows += vec ? (q.heads + 32 / lpr - 1) / (32 / lpr) : q.heads;
-  }
-  if (!vec) {
-    rows = 0;
-    for (int i = 0; i < p.parts; ++i) rows += p.part[i].heads;
+    rows += q.heads;
   }
   const long long tokens = (long long)p.B * p.N;
+  if (vec) {
+    // as many tokens a CTA as leave every SM some CTAs, up to the room for their angles
+    const long long most = kAngleFloats / p.D < 32 ? kAngleFloats / p.D : 32;
+    long long tile = tokens / ((long long)sms * 8);
+    tile = tile < 1 ? 1 : (tile > most ? most : tile);
+    p.tile = (int)(tile < p.N ? tile : p.N);
+    p.tiles = (p.N + p.tile - 1) / p.tile;
+    const unsigned ctas = (unsigned)((long long)p.tiles * p.B);
+    if (half)
+      launch_vec<T, true>(p, ctas, st);
+    else
+      launch_vec<T, false>(p, ctas, st);
+    return cudaGetLastError();
+  }
   // few tokens: spread a token's heads over warps until the card has some for every
   // scheduler; each then computes the token's angles again
   const long long want = (long long)sms * 16;
@@ -383,10 +487,7 @@ cudaError_t launch_typed(TokenParams &p, int sms, cudaStream_t st) {
   p.tasks = tokens * p.groups;
   long long ctas = (p.tasks + kWarps - 1) / kWarps;
   if (ctas > (long long)sms * 8) ctas = (long long)sms * 8;
-  if (vec)
-    token_vec_kernel<T><<<(unsigned)ctas, kThreads, 0, st>>>(p);
-  else
-    token_elem_kernel<T><<<(unsigned)ctas, kThreads, 0, st>>>(p);
+  token_elem_kernel<T><<<(unsigned)ctas, kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 

@@ -55,6 +55,8 @@ bool queries_ok(const Dims &d, int32_t q_len) {
 bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
 // ------------------------------------------------------------ checks of the token operators
+constexpr int32_t kMaxTokenHeads = 65536;
+
 size_t dtype_bytes(int32_t dtype) {
   return dtype == RESS_BF16 || dtype == RESS_FP16 ? 2 : (dtype == RESS_FP32 ? 4 : 0);
 }
@@ -496,6 +498,7 @@ ress_status ress_rope(const ress_rope_plan *plan, int32_t batch, int32_t heads, 
   if (inverse != 0 && inverse != 1) return RESS_ERR_INVALID_ARG;
   const size_t size = dtype_bytes(dtype);
   if (size == 0 || !positions_ok(plan, positions, pos_stride_b)) return RESS_ERR_INVALID_ARG;
+  if (heads > kMaxTokenHeads) return RESS_ERR_UNSUPPORTED;
   if (batch == 0 || heads == 0 || tokens == 0) return RESS_OK;
   if (!rows_ok(x, size) || !out_rows_ok(out, size, batch, heads, tokens, plan->head_dim))
     return RESS_ERR_INVALID_ARG;
@@ -537,6 +540,7 @@ ress_status ress_qk_norm_rope(const ress_qk_params *params, const ress_rows *q,
   if (p.views < 1 || p.specials < 0 || p.tokens % p.views != 0 || p.specials > p.tokens / p.views)
     return RESS_ERR_INVALID_ARG;
   if ((v == nullptr) != (v_out == nullptr)) return RESS_ERR_INVALID_ARG;
+  if (p.q_heads > kMaxTokenHeads || p.kv_heads > kMaxTokenHeads) return RESS_ERR_UNSUPPORTED;
   if (p.batch == 0 || p.tokens == 0) return RESS_OK;
   const bool moves = p.specials > 0 && p.specials < p.tokens / p.views;  // some token's place changes
   const ress_rows *in[3] = {q, k, v}, *out[3] = {q_out, k_out, v_out};

@@ -467,7 +467,8 @@ typedef struct {
  * A the plan's amplitude.  inverse = 1 turns by -w (the transposed map: the gradient of the
  * forward call, and its inverse where A = 1).  fp32 arithmetic from the stored type,
  * rounded once.  w is reduced exactly: an angle is as precise at position 2^30 as at 1.
- *   batch, heads, tokens >= 0: x and out are [batch, heads, tokens, plan->head_dim].
+ *   batch, heads, tokens >= 0: x and out are [batch, heads, tokens, plan->head_dim]; more
+ *   than 65536 heads are UNSUPPORTED.
  *   dtype: ress_dtype of x and out.
  *   positions  DEVICE int32 [batch or 1][tokens][axes], any sign, 4-byte aligned;
  *              pos_stride_b: elements from one batch entry's to the next (0: shared).
@@ -483,7 +484,7 @@ ress_status ress_rope(const ress_rope_plan *plan, int32_t batch, int32_t heads, 
 
 typedef struct {
   int32_t batch, tokens;       /* >= 0 */
-  int32_t q_heads, kv_heads;   /* >= 1 */
+  int32_t q_heads, kv_heads;   /* 1..65536 */
   int32_t head_dim;            /* 2..256 */
   int32_t dtype;               /* ress_dtype of every tensor */
   int32_t norm;                /* ress_norm, over the head_dim elements of each row */

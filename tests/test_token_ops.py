@@ -22,7 +22,7 @@ from block_sparse_global_b200 import workload as W
 from block_sparse_global_b200.pipeline import SparseGlobalAttention
 from oracle import token_oracle as T
 
-INVALID, OK = 1, 0
+INVALID, UNSUPPORTED, OK = 1, 2, 0
 FAKE = 0x7F0000000000
 U = 2.0 ** -24
 BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
@@ -101,6 +101,7 @@ def test_rope_refusals(lib):
     bad = R.rope_plan(64)
     bad.amplitude = 0.0
     assert call(plan=bad) == INVALID
+    assert call(H=65537, out=_view(FAKE + 65536, t=64 * 65537)) == UNSUPPORTED
     assert call(N=0, x=_view(None), out=_view(None)) == OK           # empty: nothing is looked at
     assert call(B=0) == OK and call(H=0) == OK
 
@@ -127,6 +128,7 @@ def test_qk_refusals(lib):
     # in place is for calls that keep the token order, and for equal strides
     assert call(q_out=_view(), specials=2) == INVALID
     assert call(q_out=_view(h=1280, t=64)) == INVALID
+    assert call(q_heads=65537) == UNSUPPORTED and call(kv_heads=65537) == UNSUPPORTED
     assert call(batch=0) == OK and call(tokens=0) == OK
 
 
