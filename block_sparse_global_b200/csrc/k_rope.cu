@@ -127,11 +127,16 @@ RESS_DEV float row_sum(float v, int lanes) {
 // chunks half a section apart in the half layout, neighbours in the interleaved one.  A row
 // takes D / 2V lanes, rounded up to a power of two (the rest idle), and a warp's pass several
 // heads of one token.  The passes of all tensors and the CTA's tokens form one list, pass by
-// pass, of which each warp takes an equal stretch, with the loads of the next pieces in
-// flight; weights and biases stay in registers until the tensor changes.
+// pass, of which each warp takes an equal stretch: a few runs of tokens of one pass, in which
+// pointers advance, weights and biases stay in registers and kPieces tokens' loads are in
+// flight.
 // Both sums of the layer norm are over centred values, in fp32.
 constexpr int kAngleFloats = 4096;  // (cos, sin) of the CTA's tokens: 16 KB
-constexpr int kPieces = 4;          // pieces in flight per warp
+// CTAs of an SM: the norm needs 128 registers; the rotation alone lives with 80 and gains from
+// more loads in flight (100 views: 110 us with three CTAs, 133 us with two).
+constexpr int kCtasRotate = 3, kCtasNorm = 2;
+constexpr int kMaxTile = 32;        // tokens of a CTA
+constexpr int kPieces = 2;          // pieces worked on, and as many in flight behind them
 
 RESS_DEV uint64_t pk2(float lo, float hi) {
   return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
@@ -201,33 +206,16 @@ RESS_DEV uint4 repack<__half>(const uint64_t *x) {
 
 // HALF: the pair layout; NORM: ress_norm.
 template <typename T, bool HALF, int NORM>
-__global__ void __launch_bounds__(kThreads) token_vec_kernel(const __grid_constant__ TokenParams p) {
+__global__ void __launch_bounds__(kThreads, NORM == RESS_NORM_NONE ? kCtasRotate : kCtasNorm)
+    token_vec_kernel(const __grid_constant__ TokenParams p) {
   constexpr int V = 16 / sizeof(T);  // elements of a chunk
   __shared__ __align__(16) float cs[kAngleFloats];
   __shared__ __align__(16) float wb[4][kMaxDim];
+  __shared__ int to[kMaxTile];  // rows that the tokens go to
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / p.tiles, t0 = (blockIdx.x - b * p.tiles) * p.tile;
   const int nt = min(p.tile, p.N - t0);
   const int pairs = p.rot >> 1, slots = p.D >> 1;  // cos, then sin, of `slots` pairs a token
-  if (pairs > 0) {
-    const int per = pairs / p.axes;
-    for (int i = tid; i < nt * pairs; i += kThreads) {
-      const int t = i / pairs, k = i - t * pairs, a = k / per;
-      const float2 v = pair_angle(p, p.phase[k - a * per], b, t0 + t, a);
-      cs[2 * slots * t + k] = v.x;
-      cs[2 * slots * t + slots + k] = v.y;
-    }
-  }
-  if (NORM != RESS_NORM_NONE) {
-    for (int i = tid; i < p.D; i += kThreads) {
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        wb[2 * a][i] = p.part[a].weight ? p.part[a].weight[i] : 1.f;
-        wb[2 * a + 1][i] = p.part[a].bias ? p.part[a].bias[i] : 0.f;
-      }
-    }
-  }
-  __syncthreads();
   const int used = p.D / (2 * V);  // lanes of a row that hold something
   int lpr = 1;
   while (lpr < used) lpr <<= 1;
@@ -245,96 +233,145 @@ __global__ void __launch_bounds__(kThreads) token_vec_kernel(const __grid_consta
   const int it1 = (p.part[0].heads + rpw - 1) / rpw;
   const int it2 = it1 + (p.parts > 1 ? (p.part[1].heads + rpw - 1) / rpw : 0);
   const int its = it2 + (p.parts > 2 ? (p.part[2].heads + rpw - 1) / rpw : 0);
+  const float inv_d = 1.0f / p.D;
   const int i0 = its * nt * warp / kWarps, i1 = its * nt * (warp + 1) / kWarps;
-  int cur = -1;              // tensor of the weights in registers
-  uint64_t w[V], bias[V];    // V / 2 pairs of chunk a, then of chunk b
-  for (int i = i0; i < i1; i += kPieces) {
-    uint4 raw[kPieces][2];
+  // the run of pieces that is being worked on
+  int which = 0, ta = 0, tb = 0;
+  bool there = false;
+  const T *src = nullptr;
+  T *dst = nullptr;
+  uint4 next[kPieces][2];
+  auto load = [&](int t) {
+    const long long in_t = p.part[which].in_t;
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
-      const int pass = (i + u) / nt, t = i + u - pass * nt;
-      const int which = pass < it1 ? 0 : (pass < it2 ? 1 : 2);
-      const Part &q = p.part[which];
-      const int h = (pass - (which == 0 ? 0 : (which == 1 ? it1 : it2))) * rpw + sub;
-      raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
-      if (i + u < i1 && holds && h < q.heads) {
-        const T *src = static_cast<const T *>(q.in) + b * q.in_b + h * q.in_h + (t0 + t) * q.in_t;
-        raw[u][0] = *reinterpret_cast<const uint4 *>(src + ca);
-        raw[u][1] = *reinterpret_cast<const uint4 *>(src + cb);
+      next[u][0] = next[u][1] = make_uint4(0, 0, 0, 0);
+      if (there && t + u < tb) {
+        next[u][0] = *reinterpret_cast<const uint4 *>(src + ca);
+        next[u][1] = *reinterpret_cast<const uint4 *>(src + cb);
+      }
+      src += in_t;
+    }
+  };
+  auto open = [&](int i) {
+    const int pass = i / nt;
+    ta = i - pass * nt;
+    tb = min(nt, ta + i1 - i);
+    which = pass < it1 ? 0 : (pass < it2 ? 1 : 2);
+    const Part &q = p.part[which];
+    const int h = (pass - (which == 0 ? 0 : (which == 1 ? it1 : it2))) * rpw + sub;
+    there = holds && h < q.heads;
+    src = static_cast<const T *>(q.in) + b * q.in_b + h * q.in_h + (t0 + ta) * q.in_t;
+    dst = static_cast<T *>(q.out) + b * q.out_b + h * q.out_h;
+    load(ta);
+  };
+  if (i0 < i1) open(i0);  // its loads are under way while the angles are computed
+  if (pairs > 0) {
+    const int per = pairs / p.axes;
+    for (int i = tid; i < nt * pairs; i += kThreads) {
+      const int t = i / pairs, k = i - t * pairs, a = k / per;
+      const float2 v = pair_angle(p, p.phase[k - a * per], b, t0 + t, a);
+      cs[2 * slots * t + k] = v.x;
+      cs[2 * slots * t + slots + k] = v.y;
+    }
+  }
+  if (tid < nt) to[tid] = target_row(p, t0 + tid);
+  if (NORM != RESS_NORM_NONE) {
+    for (int i = tid; i < p.D; i += kThreads) {
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        wb[2 * a][i] = p.part[a].weight ? p.part[a].weight[i] : 1.f;
+        wb[2 * a + 1][i] = p.part[a].bias ? p.part[a].bias[i] : 0.f;
       }
     }
+  }
+  __syncthreads();
+  for (int i = i0; i < i1;) {
+    i += tb - ta;
+    const long long out_t = p.part[which].out_t;
+    const bool work = p.part[which].work;
+    uint64_t w[V], bias[V];  // V / 2 pairs of chunk a, then of chunk b
+    if (NORM != RESS_NORM_NONE && work) {
+      const int ra = holds ? ca : 0, rb = holds ? cb : 0;
 #pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      if (i + u >= i1) break;
-      const int pass = (i + u) / nt, t = i + u - pass * nt;
-      const int which = pass < it1 ? 0 : (pass < it2 ? 1 : 2);
-      const Part &q = p.part[which];
-      const int h = (pass - (which == 0 ? 0 : (which == 1 ? it1 : it2))) * rpw + sub;
-      if (q.work) {
-        uint64_t x[V];
-        unpack<T>(raw[u][0], x);
-        unpack<T>(raw[u][1], x + V / 2);
-        if (NORM != RESS_NORM_NONE) {
-          if (which != cur) {
-            cur = which;
-            const int ra = holds ? ca : 0, rb = holds ? cb : 0;
+      for (int e = 0; e < V / 2; ++e) {
+        w[e] = *reinterpret_cast<const uint64_t *>(&wb[2 * which][ra + 2 * e]);
+        w[V / 2 + e] = *reinterpret_cast<const uint64_t *>(&wb[2 * which][rb + 2 * e]);
+        bias[e] = *reinterpret_cast<const uint64_t *>(&wb[2 * which + 1][ra + 2 * e]);
+        bias[V / 2 + e] = *reinterpret_cast<const uint64_t *>(&wb[2 * which + 1][rb + 2 * e]);
+      }
+    }
+    for (int t = ta; t < tb; t += kPieces) {
+      uint4 raw[kPieces][2];
 #pragma unroll
-            for (int e = 0; e < V / 2; ++e) {
-              w[e] = *reinterpret_cast<const uint64_t *>(&wb[2 * which][ra + 2 * e]);
-              w[V / 2 + e] = *reinterpret_cast<const uint64_t *>(&wb[2 * which][rb + 2 * e]);
-              bias[e] = *reinterpret_cast<const uint64_t *>(&wb[2 * which + 1][ra + 2 * e]);
-              bias[V / 2 + e] = *reinterpret_cast<const uint64_t *>(&wb[2 * which + 1][rb + 2 * e]);
+      for (int u = 0; u < kPieces; ++u) {
+        raw[u][0] = next[u][0];
+        raw[u][1] = next[u][1];
+      }
+      load(t + kPieces);
+#pragma unroll
+      for (int u = 0; u < kPieces; ++u) {
+        if (t + u >= tb) break;
+        if (work) {
+          uint64_t x[V];
+          unpack<T>(raw[u][0], x);
+          unpack<T>(raw[u][1], x + V / 2);
+          if (NORM != RESS_NORM_NONE) {
+            if (NORM == RESS_NORM_LAYER) {
+              uint64_t m = x[0];
+#pragma unroll
+              for (int e = 1; e < V; ++e) m = add2(m, x[e]);
+              const float total = row_sum(lo2(m) + hi2(m), lpr);
+              const float mean = holds ? total * inv_d : 0.f;  // idle lanes stay 0
+              const uint64_t m2 = pk2(-mean, -mean);
+#pragma unroll
+              for (int e = 0; e < V; ++e) x[e] = add2(x[e], m2);
             }
+            uint64_t ss = mul2(x[0], x[0]);
+#pragma unroll
+            for (int e = 1; e < V; ++e) ss = fma2(x[e], x[e], ss);
+            const float r = rsqrtf(fmaf(row_sum(lo2(ss) + hi2(ss), lpr), inv_d, p.eps));
+            const uint64_t r2 = pk2(r, r);
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[e] = fma2(mul2(x[e], r2), w[e], bias[e]);
           }
-          if (NORM == RESS_NORM_LAYER) {
-            uint64_t m = x[0];
+          if (turned) {
+            const float *c = cs + 2 * slots * (t + u) + own * V, *s = c + slots;
 #pragma unroll
-            for (int e = 1; e < V; ++e) m = add2(m, x[e]);
-            const float total = row_sum(lo2(m) + hi2(m), lpr);
-            const float mean = holds ? total / p.D : 0.f;  // idle lanes stay 0
-            const uint64_t m2 = pk2(-mean, -mean);
+            for (int e = 0; e < V / 2; e += 2) {
+              const ulonglong2 ce2 = *reinterpret_cast<const ulonglong2 *>(c + 2 * e);
+              const ulonglong2 se2 = *reinterpret_cast<const ulonglong2 *>(s + 2 * e);
 #pragma unroll
-            for (int e = 0; e < V; ++e) x[e] = add2(x[e], m2);
-          }
-          uint64_t ss = mul2(x[0], x[0]);
+              for (int f = 0; f < 2; ++f) {
+                const uint64_t ce = f ? ce2.y : ce2.x, se = f ? se2.y : se2.x;
+                if (HALF) {  // pairs (x_a, x_b)
+                  const uint64_t ns = se ^ 0x8000000080000000ull;
+                  const uint64_t a = x[e + f], d = x[V / 2 + e + f];
+                  x[e + f] = fma2(d, ns, mul2(a, ce));
+                  x[V / 2 + e + f] = fma2(a, se, mul2(d, ce));
+                } else {  // pairs inside the packed values
 #pragma unroll
-          for (int e = 1; e < V; ++e) ss = fma2(x[e], x[e], ss);
-          const float r = rsqrtf(row_sum(lo2(ss) + hi2(ss), lpr) / p.D + p.eps);
-          const uint64_t r2 = pk2(r, r);
-#pragma unroll
-          for (int e = 0; e < V; ++e) x[e] = fma2(mul2(x[e], r2), w[e], bias[e]);
-        }
-        if (turned) {
-          const uint64_t *c = reinterpret_cast<const uint64_t *>(cs + 2 * slots * t + own * V);
-          const uint64_t *s = c + slots / 2;
-#pragma unroll
-          for (int e = 0; e < V / 2; ++e) {
-            const uint64_t ce = c[e], se = s[e];
-            if (HALF) {  // pairs (x_a, x_b)
-              const uint64_t ns = se ^ 0x8000000080000000ull;
-              const uint64_t a = x[e], d = x[V / 2 + e];
-              x[e] = fma2(d, ns, mul2(a, ce));
-              x[V / 2 + e] = fma2(a, se, mul2(d, ce));
-            } else {  // pairs inside the packed values
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                if (own * V + 2 * e + k >= pairs) continue;
-                const float cc = k ? hi2(ce) : lo2(ce), sn = k ? hi2(se) : lo2(se);
-                const float a = lo2(x[2 * e + k]), d = hi2(x[2 * e + k]);
-                x[2 * e + k] = pk2(fmaf(-d, sn, a * cc), fmaf(a, sn, d * cc));
+                  for (int k = 0; k < 2; ++k) {
+                    if (own * V + 2 * (e + f) + k >= pairs) continue;
+                    const float cc = k ? hi2(ce) : lo2(ce), sn = k ? hi2(se) : lo2(se);
+                    const float a = lo2(x[2 * (e + f) + k]), d = hi2(x[2 * (e + f) + k]);
+                    x[2 * (e + f) + k] = pk2(fmaf(-d, sn, a * cc), fmaf(a, sn, d * cc));
+                  }
+                }
               }
             }
           }
+          raw[u][0] = repack<T>(x);
+          raw[u][1] = repack<T>(x + V / 2);
         }
-        raw[u][0] = repack<T>(x);
-        raw[u][1] = repack<T>(x + V / 2);
-      }
-      if (holds && h < q.heads) {
-        T *dst = static_cast<T *>(q.out) + b * q.out_b + h * q.out_h + target_row(p, t0 + t) * q.out_t;
-        *reinterpret_cast<uint4 *>(dst + ca) = raw[u][0];
-        *reinterpret_cast<uint4 *>(dst + cb) = raw[u][1];
+        if (there) {
+          T *row = dst + to[t + u] * out_t;
+          *reinterpret_cast<uint4 *>(row + ca) = raw[u][0];
+          *reinterpret_cast<uint4 *>(row + cb) = raw[u][1];
+        }
       }
     }
+    if (i < i1) open(i);
   }
 }
 
@@ -466,10 +503,11 @@ cudaError_t launch_typed(TokenParams &p, int sms, cudaStream_t st) {
   }
   const long long tokens = (long long)p.B * p.N;
   if (vec) {
-    // as many tokens a CTA as leave every SM some CTAs, up to the room for their angles
-    const long long most = kAngleFloats / p.D < 32 ? kAngleFloats / p.D : 32;
-    long long tile = tokens / ((long long)sms * 8);
-    tile = tile < 1 ? 1 : (tile > most ? most : tile);
+    // full waves of resident CTAs, of as many tokens as their angles have room for
+    const long long most = kAngleFloats / p.D < kMaxTile ? kAngleFloats / p.D : kMaxTile;
+    const long long wave = (long long)sms * (p.norm == RESS_NORM_NONE ? kCtasRotate : kCtasNorm);
+    const long long waves = (tokens + most * wave - 1) / (most * wave);
+    const long long tile = (tokens + waves * wave - 1) / (waves * wave);
     p.tile = (int)(tile < p.N ? tile : p.N);
     p.tiles = (p.N + p.tile - 1) / p.tile;
     const unsigned ctas = (unsigned)((long long)p.tiles * p.B);
