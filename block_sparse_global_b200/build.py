@@ -14,9 +14,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libress.so")
 SOURCES = ["ress_api.cu", "k_blocks.cu", "k_select.cu", "k_attn.cu", "k_masked_attn.cu",
-           "k_rope.cu"]
+           "k_masked_step.cu", "k_rope.cu"]
 HEADERS = ["ress_common.cuh", "ress_internal.h", "k_tiles.cuh", "k_topk.cuh",
-           "k_attn.cuh"]
+           "k_attn.cuh", "k_masked.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -34,7 +34,7 @@
 #include <climits>
 
 #include "k_attn.cuh"
-#include "ress_internal.h"
+#include "k_masked.cuh"
 
 namespace ress {
 namespace {
@@ -44,7 +44,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kProducerWarp = 4;
 constexpr int kMmaWarp = 5;
 constexpr float kRescaleLog2 = 8.0f;  // O and l are rescaled when the max grows by more
-constexpr float kNoMax = -3.0e38f;    // running max of a row that has seen no key
 constexpr int kKStages = 3;
 constexpr int kVStages = 2;
 constexpr int kTile = 128 * 64 * 2;  // bytes of one 128 x 64 bf16 tile
@@ -62,8 +61,6 @@ constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 192;
 constexpr int kUneven = INT_MIN;  // step of a block whose positions do not run evenly
 constexpr uint32_t kWhole = 0, kMixed = 1, kNone = 2;  // what a warp sees of a block
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.69314718055994530942f;
 
 struct Bars {
   uint64_t q_full;
@@ -89,31 +86,7 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 384, "barriers fit their shared-memory slot");
 
-RESS_DEV float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 RESS_DEV void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-RESS_DEV uint64_t fmul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
-// tanh(y) / y as a polynomial in y^2, fitted here for minimax relative error (Lawson's
-// iteratively reweighted least squares): up to |y| = 3/8 (degree 3, 5.9e-8), up to 1/2
-// (degree 4, 1.3e-8; 1.1e-7 evaluated in fp32) and up to 1 (degree 6, 5e-8; 1.6e-7).
-constexpr double kTanhFit3[4] = {9.999999404e-01, -3.333197534e-01, 1.328450292e-01, -4.827226326e-02};
-template <int N>
-RESS_DEV constexpr float tanh_fit(int k) {
-  constexpr float c4[5] = {1.000000000e+00f, -3.333306909e-01f, 1.332477927e-01f, -5.298607424e-02f,
-                           1.713500544e-02f};
-  constexpr float c6[7] = {9.999999404e-01f, -3.333283961e-01f, 1.332520396e-01f, -5.345702916e-02f,
-                           2.028998174e-02f, -6.203379016e-03f, 1.041022479e-03f};
-  return N == 4 ? c4[k < 5 ? k : 4] : c6[k];
-}
 
 // s <- tanh(s in) of a row's 128 scores, by the polynomial.
 template <int N>
@@ -131,17 +104,11 @@ RESS_DEV void cap_small(uint32_t (&sv)[128], float in) {
     sv[c + 1] = __float_as_uint(f2hi(u));
   }
 }
-// Any score: 1 - 2 / (1 + e^2y) is off by an fp32 unit absolutely, the polynomial below
-// |y| = 1/2 relatively.
+// Any score.
 RESS_DEV void cap_any(uint32_t (&sv)[128], float in) {
 #pragma unroll
   for (int c = 0; c < 128; ++c) {
-    const float y = __uint_as_float(sv[c]) * in, t = y * y;
-    float a = tanh_fit<4>(4);
-#pragma unroll
-    for (int k = 3; k >= 0; --k) a = fmaf(a, t, tanh_fit<4>(k));
-    const float r = rcp_approx(1.0f + ex2_approx(2.0f * kLog2e * y));
-    sv[c] = __float_as_uint(fabsf(y) < 0.5f ? a * y : fmaf(-2.0f, r, 1.0f));
+    sv[c] = __float_as_uint(tanh_any(__uint_as_float(sv[c]) * in));
   }
 }
 
@@ -1042,6 +1009,7 @@ cudaError_t launch_masked_attn(const Dims &d, const MaskedAttnLaunch &a, cudaStr
     no_keys_kernel<<<(unsigned)ctas, 256, 0, st>>>(rows, static_cast<uint4 *>(a.out), a.lse);
     return cudaGetLastError();
   }
+  if (masked_step_fits(d, Nq)) return launch_masked_step(d, a, st);
   CUtensorMap mq, mk, mv;
   if (!make_map(&mq, a.q, Nq, d.BH(), 128) || !make_map(&mk, a.k, d.N, d.BH(), d.kb) ||
       !make_map(&mv, a.v, d.N, d.BH(), d.kb))

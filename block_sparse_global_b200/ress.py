@@ -338,14 +338,13 @@ def rope_plan(head_dim: int, rot_dim: Optional[int] = None, axes: int = 1, layou
     return plan
 
 
-def _rows(t: torch.Tensor, like=None) -> ress_rows:
-    """A [B, heads, N, D] tensor as strided rows; `like` = (shape, dtype, device) to match."""
-    if t.dim() != 4:
-        raise ValueError("expected a [batch, heads, tokens, head_dim] tensor")
-    if like is not None and (t.shape, t.dtype, t.device) != like:
-        raise ValueError(f"expected {like}, got {(t.shape, t.dtype, t.device)}")
+def _rows(t: torch.Tensor, shape, dtype, device) -> ress_rows:
+    """A [B, heads, N, D] tensor of this shape, type and device as strided rows."""
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"expected {dtype} {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
     b, h, n, e = t.stride()
-    if e != 1 and t.shape[3] > 1:
+    if e != 1 and shape[3] > 1:
         raise ValueError("the elements of a row must be contiguous")
     return ress_rows(t.data_ptr() or None, b, h, n)
 
@@ -359,6 +358,8 @@ def _positions(plan, positions, batch: int, tokens: int, device):
         raise ValueError("positions must be int32 on the tensors' device")
     axes = plan.axes
     p = positions
+    if p.dim() == 3 and p.shape == (batch, tokens, axes) and p.is_contiguous():
+        return p.data_ptr() or None, tokens * axes
     if axes == 1 and p.dim() <= 2 and (p.dim() == 1 or p.shape[-1] == tokens and p.shape[0] in (1, batch)):
         p = p.unsqueeze(-1)
     if p.dim() == 2:
@@ -391,21 +392,22 @@ def _launch(name: str, device, stream, *args):
 def ress_rope(plan, x: torch.Tensor, positions: Optional[torch.Tensor], out: torch.Tensor,
               inverse: bool = False, stream=None):
     """Rotates x [B, heads, N, D] (any strides over whole rows) into out (may be x)."""
-    if x.shape[-1] != plan.head_dim or x.dtype not in DTYPES:
-        raise ValueError(f"expected rows of {plan.head_dim} bf16, fp16 or fp32 elements")
-    src, dst = _rows(x), _rows(out, (x.shape, x.dtype, x.device))
-    b, h, n, _ = x.shape
-    pos, pos_b = _positions(plan, positions, b, n, x.device)
-    _launch("ress_rope", x.device, stream, ctypes.byref(plan), b, h, n, DTYPES[x.dtype],
-            ctypes.byref(src), pos, pos_b, 1 if inverse else 0, ctypes.byref(dst))
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    if len(shape) != 4 or shape[3] != plan.head_dim or dtype not in DTYPES:
+        raise ValueError(f"expected [B, heads, N, {plan.head_dim}] of bf16, fp16 or fp32")
+    src, dst = _rows(x, shape, dtype, dev), _rows(out, shape, dtype, dev)
+    b, h, n, _ = shape
+    pos, pos_b = _positions(plan, positions, b, n, dev)
+    _launch("ress_rope", dev, stream, plan, b, h, n, DTYPES[dtype], src, pos, pos_b,
+            1 if inverse else 0, dst)
 
 
 def _affine(w: Optional[torch.Tensor], dim: int, device):
     if w is None:
         return None
-    if w.dtype != torch.float32 or w.shape != (dim,) or w.device != device:
+    if w.dtype != torch.float32 or w.shape != (dim,) or w.device != device or not w.is_contiguous():
         raise ValueError(f"norm weights and biases must be fp32 [{dim}] on the tensors' device")
-    return _ptr(w)
+    return w.data_ptr()
 
 
 def ress_qk_norm_rope(q, k, q_out, k_out, v=None, v_out=None, norm: int = NORM_RMS,
@@ -413,23 +415,23 @@ def ress_qk_norm_rope(q, k, q_out, k_out, v=None, v_out=None, norm: int = NORM_R
                       plan=None, positions=None, views: int = 1, specials: int = 0, stream=None):
     """Per-head norm and rotation of q and k (and the move of v) in one pass, into the token
     order of ress_token_gather.  Tensors are [B, heads, N, D] views of any strides."""
-    if q.dim() != 4 or k.dim() != 4 or q.dtype not in DTYPES:
+    shape, dtype, dev = q.shape, q.dtype, q.device
+    if len(shape) != 4 or k.dim() != 4 or dtype not in DTYPES:
         raise ValueError("expected [batch, heads, tokens, head_dim] tensors of bf16, fp16 or fp32")
     if (v is None) != (v_out is None):
         raise ValueError("v and v_out go together")
-    b, h, n, d = q.shape
-    g = k.shape[1]
-    kv = (torch.Size((b, g, n, d)), q.dtype, q.device)
-    rows = [_rows(q), _rows(k, kv), None if v is None else _rows(v, kv),
-            _rows(q_out, (q.shape, q.dtype, q.device)), _rows(k_out, kv),
-            None if v_out is None else _rows(v_out, kv)]
-    pos, pos_b = (None, 0) if plan is None else _positions(plan, positions, b, n, q.device)
-    aff = [_affine(w, d, q.device) for w in (q_weight, q_bias, k_weight, k_bias)]
-    p = ress_qk_params(b, n, h, g, d, DTYPES[q.dtype], int(norm), float(eps), *aff,
-                       ctypes.pointer(plan) if plan is not None else None, pos, pos_b, int(views),
-                       int(specials))
-    _launch("ress_qk_norm_rope", q.device, stream, ctypes.byref(p),
-            *[None if r is None else ctypes.byref(r) for r in rows])
+    b, h, n, d = shape
+    kv = k.shape
+    if kv[0] != b or kv[2] != n or kv[3] != d:
+        raise ValueError(f"q {tuple(shape)} and k {tuple(kv)} do not belong together")
+    pos, pos_b = (None, 0) if plan is None else _positions(plan, positions, b, n, dev)
+    p = ress_qk_params(b, n, h, kv[1], d, DTYPES[dtype], norm, eps, _affine(q_weight, d, dev),
+                       _affine(q_bias, d, dev), _affine(k_weight, d, dev), _affine(k_bias, d, dev),
+                       None if plan is None else ctypes.pointer(plan), pos, pos_b, views, specials)
+    _launch("ress_qk_norm_rope", dev, stream, p, _rows(q, shape, dtype, dev),
+            _rows(k, kv, dtype, dev), None if v is None else _rows(v, kv, dtype, dev),
+            _rows(q_out, shape, dtype, dev), _rows(k_out, kv, dtype, dev),
+            None if v_out is None else _rows(v_out, kv, dtype, dev))
 
 
 # ------------------------------------------------------- attention with changed scores

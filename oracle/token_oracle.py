@@ -125,7 +125,7 @@ def masked_attn(q, k, v, scale, key_block=128, kv_lists=None, softcap=0.0, slope
             ok = torch.where(fin[:, None], vv, torch.zeros_like(vv))
             out[b, h] = w @ ok
             size[b, h] = w @ ok.abs()
-            for u in torch.nonzero(~fin).flatten().tolist():
+            for u in torch.nonzero(~fin & any_).flatten().tolist():
                 rows = vis[:, u]
                 out[b, h, rows] += w[rows, u, None] * vv[u]
                 size[b, h, rows] += w[rows, u, None] * vv[u].abs()

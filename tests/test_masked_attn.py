@@ -277,7 +277,7 @@ def test_plain_call_agrees_with_the_unmasked_kernel():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kb", [64, 128])
-@pytest.mark.parametrize("Nq", [400, 3])
+@pytest.mark.parametrize("Nq", [400, 3, 1])
 def test_hidden_keys_hold_anything(kb, Nq):
     """Infinities and NaN in keys and values that the masks hide do not change a bit of the
     other rows; where a row sees them, its output says so; padded queries may hold them too."""
@@ -336,6 +336,30 @@ def test_rows_without_keys(N, Nq):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kb", [64, 128])
+@pytest.mark.parametrize("Bn,H,N", [(1, 1, 1), (1, 1, 70), (2, 3, 129), (1, 16, 2500), (5, 16, 1111), (20, 16, 300),
+                                    (1, 8, 20001), (1, 2, 30000)])
+@pytest.mark.parametrize("what", ["plain", "masks", "bias"])
+def test_single_tokens(Bn, H, N, kb, what):
+    """One query per head: lists in any order, masks in any order, values hidden or not."""
+    torch.manual_seed(N + H)
+    q, k, v, g = _inputs(Bn, H, N, 1, seed=N + Bn, size=1.5)
+    lists = _lists(Bn, H, 1, N, kb, 0.6, g) if what != "bias" else None
+    mods, cap = {}, 0.0
+    if what == "masks":
+        mods = _arrays(Bn, N, 1, 2, N // 9, "view", 0.0, H, g, shuffle=True)
+        mods["q_doc"] = torch.zeros(Bn, 1, dtype=torch.int32, device="cuda")
+        hide = mods["k_doc"] != 0
+        k = torch.where(hide[:, None, :, None], torch.full_like(k, float("nan")), k)
+        v = torch.where(hide[:, None, :, None], torch.full_like(v, float("inf")), v)
+        cap = 8.0
+    elif what == "bias":
+        mods = _arrays(Bn, N, 1, 0, 0, "none", 0.02, H, g)
+    out, lse = _run(q, k, v, kb, lists, softcap=cap, **mods)
+    _check(q, k, v, out, lse, kb, lists, softcap=cap, **mods)
+
+
+@pytest.mark.gpu
 def test_a_block_listed_twice_counts_twice():
     q, k, v, g = _inputs(1, 2, 640, 640, seed=2)
     lists = {(0, h, i): [1, 3, 1] if h else [4, 4, 4, 0, 4] for h in range(2) for i in range(5)}
@@ -344,7 +368,7 @@ def test_a_block_listed_twice_counts_twice():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("Nq", [600, 2])
+@pytest.mark.parametrize("Nq", [600, 2, 1])
 def test_bad_lists_set_the_error_and_leave_the_row(Nq):
     """An index or a count out of range is found by the kernel's own check before any load."""
     N = 600 if Nq == 600 else 1100                # the second in parts that are joined
