@@ -112,6 +112,12 @@ RESS_DEV void cap_any(uint32_t (&sv)[128], float in) {
   }
 }
 
+// Programmatic dependent launch: a kernel's CTAs may start while the kernel before it still
+// runs, once all of that one's CTAs have called launch_dependents (or ended), and wait for its
+// results where they need them.  Without the launch attribute both do nothing.
+RESS_DEV void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+RESS_DEV void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct Params {
   const int32_t *kv_idx, *kv_cnt, *order;
   const int32_t *q_pos, *k_pos, *q_doc, *k_doc, *q_order, *k_order;
@@ -147,19 +153,29 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   // rows of a head from its last query block to its first: under an order mask the long
   // rows start first, and a head's keys stay in L2 while its rows run
-  const long long x = blockIdx.x;
-  const long long item = p.order ? (long long)p.order[x] : x / p.nq * p.nq + (p.nq - 1 - (int)(x % p.nq));
-  const long long bh = item / p.nq;
-  const int qi = (int)(item - bh * p.nq);
-  const int b = (int)(bh / p.H);
+  launch_dependents();
+  if (p.order) wait_prerequisites();  // (an order of our own is written by the kernel before)
+  const int x = blockIdx.x;
+  const int item32 = p.order ? p.order[x] : x / p.nq * p.nq + (p.nq - 1 - x % p.nq);
+  const int bh = item32 / p.nq, qi = item32 - bh * p.nq, b = bh / p.H;
+  const long long item = item32;
   const bool masked = p.q_doc != nullptr || p.q_order != nullptr;
 
   // softmax warps that hold a query (the others stay out: their rows of S, P and O are
   // never read)
   const int active = min(4, (p.Nq - qi * 128 + 31) >> 5);
 
-  if (tid == 0) {
+  if (tid == kProducerWarp * 32) {
+    // the queries load while the row's blocks are looked up
     mbar_init(&bar->q_full, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
+    mbar_arrive_expect_tx(&bar->q_full, kTile);
+    tma_load_3d(smem + kOffQ, &tmQ, &bar->q_full, 0, qi * 128, bh);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (tid == 0) {
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(&bar->k_full[s], 1);
       mbar_init(&bar->k_empty[s], 1);
@@ -204,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < 5; ++i) bar->qsum[warp][i] = v[i];
   }
   __syncthreads();
+  wait_prerequisites();  // the summaries
   const int cnt = p.kv_cnt ? p.kv_cnt[item] : p.nk;
   const int32_t *kvrow = p.kv_idx ? p.kv_idx + item * p.nk : nullptr;
   const bool ragged = p.N % KB != 0;
@@ -273,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint16_t *mine = list + skip;
     if (tid == 0) {
       bar->b = b;
-      bar->bh = (int)bh;
+      bar->bh = bh;
       bar->qi = qi;
       bar->active = active;
       bar->skip = skip;
@@ -292,23 +309,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (warp == kProducerWarp) {
         // ---------------------------------------------------------- TMA producer
         if (lane == 0) {
-          if (pass == 0) {
-            tma_prefetch_desc(&tmQ);
-            tma_prefetch_desc(&tmK);
-            tma_prefetch_desc(&tmV);
-            mbar_arrive_expect_tx(&bar->q_full, kTile);
-            tma_load_3d(smem + kOffQ, &tmQ, &bar->q_full, 0, qi * 128, (int)bh);
-          }
           // one 128-row box, or two 64-row boxes (row N, past the last token, reads as zero
           // where the row has no second block)
           auto load_tile = [&](const CUtensorMap *tm, unsigned char *dst, uint64_t *full, int j) {
             mbar_arrive_expect_tx(full, kTile);
             if constexpr (KB == 128) {
-              tma_load_3d(dst, tm, full, 0, mine[j] * 128, (int)bh);
+              tma_load_3d(dst, tm, full, 0, mine[j] * 128, bh);
             } else {
               const int r1 = 2 * j + 1 < entries ? mine[2 * j + 1] * 64 : p.N;
-              tma_load_3d(dst, tm, full, 0, mine[2 * j] * 64, (int)bh);
-              tma_load_3d(dst + kTile / 2, tm, full, 0, r1, (int)bh);
+              tma_load_3d(dst, tm, full, 0, mine[2 * j] * 64, bh);
+              tma_load_3d(dst + kTile / 2, tm, full, 0, r1, bh);
             }
           };
           // tile j waits for its slot's last user, tile J - stages
@@ -346,7 +356,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_wait(&bar->k_full[(J0 + j) % kKStages], ((J0 + j) / kKStages) & 1, nullptr);
           for (int j = max(0, nv - kVStages); j < nv; ++j)
             mbar_wait(&bar->v_full[(J0 + j) % kVStages], ((J0 + j) / kVStages) & 1, nullptr);
-          mbar_wait(&bar->q_full, 0, nullptr);
         }
       } else if (warp == kMmaWarp) {
         // ---------------------------------------------------- tensor-core issuer
@@ -811,6 +820,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (p.lse) p.lse[(size_t)bh * p.Nq + t] = -INFINITY;
     }
   }
+  if (tid == kProducerWarp * 32) mbar_wait(&bar->q_full, 0, nullptr);  // whatever became of the row
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -825,6 +835,7 @@ __global__ void __launch_bounds__(256) join_kernel(const float *__restrict__ par
                                                    const float2 *__restrict__ part_ml, int splits, int nq,
                                                    int Nq, long long rows, __nv_bfloat16 *__restrict__ out,
                                                    float *__restrict__ lse) {
+  wait_prerequisites();
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
@@ -878,6 +889,7 @@ __global__ void __launch_bounds__(256) summary_kernel(const int32_t *__restrict_
                                                       const int32_t *__restrict__ order,
                                                       const int32_t *__restrict__ pos, int N, int nk, int kb,
                                                       long long blocks, int4 *__restrict__ out) {
+  launch_dependents();
   const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (i >= blocks) return;
@@ -961,13 +973,13 @@ __global__ void __launch_bounds__(256) no_keys_kernel(long long rows, uint4 *__r
 // CTAs that share a row: as many as keep the whole card (two per SM) busy, each with some
 // tiles of the longest possible row; long rows are split on into up to four times as many,
 // since kept lists and masks make them uneven (a part's sums cost 32 KB each way).
-constexpr int kSlots = 2 * 148, kTilesPerSplit = 4;
+constexpr int kSlots = 2 * 148, kTilesPerSplit = 8;
 int splits_of(const Dims &d, int nq) {
   const long long items = d.BH() * nq;
   const int tiles = (int)((d.N + 127) / 128);
   if (items == 0) return 1;
   long long n = std::max(1ll, std::min(kSlots / items, (long long)(tiles / kTilesPerSplit)));
-  while (items * n * 2 <= 4 * kSlots && tiles >= 2 * n * 4 * kTilesPerSplit) n *= 2;
+  while (items * n * 2 <= 4 * kSlots && tiles >= 2 * n * 2 * kTilesPerSplit) n *= 2;
   return (int)n;
 }
 
@@ -979,6 +991,23 @@ bool plans_order(const Dims &d, int nq) {
 }
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// A launch that may overlap the end of the kernel before it (`after`: one of this call's).
+template <typename... Sig, typename... Args>
+cudaError_t launch_after(void (*kernel)(Sig...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool after,
+                         Args... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Sig>(args)...);
+}
 
 using KernelFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const Params);
 template <int KB>
@@ -1087,12 +1116,11 @@ cudaError_t launch_masked_attn(const Dims &d, const MaskedAttnLaunch &a, cudaStr
   cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kern),
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  kern<<<dim3((unsigned)items, (unsigned)p.splits), kThreads, kSmemBytes, st>>>(mq, mk, mv, p);
-  e = cudaGetLastError();
+  e = launch_after(kern, dim3((unsigned)items, (unsigned)p.splits), kThreads, kSmemBytes, st,
+                   m.q_doc || m.q_order || m.slopes, mq, mk, mv, p);
   if (e != cudaSuccess || p.splits == 1) return e;
-  join_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p.part_o, p.part_ml, p.splits, nq, Nq, rows, p.out,
-                                                         p.lse);
-  return cudaGetLastError();
+  return launch_after(join_kernel, dim3((unsigned)((rows + 7) / 8)), 256, 0, st, true, (const float *)p.part_o,
+                      (const float2 *)p.part_ml, p.splits, nq, Nq, rows, p.out, p.lse);
 }
 
 }  // namespace ress

@@ -309,6 +309,28 @@ def test_hidden_keys_hold_anything(kb, Nq):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kb", [64, 128])
+def test_hidden_keys_in_joined_parts(kb):
+    """The same where parts of a row are joined: only the part that holds them walks again."""
+    N, Nq = 9000, 200
+    q, k, v, g = _inputs(1, 3, N, Nq, seed=17)
+    mods = _arrays(1, N, Nq, 0, 0, "view", 0.0, 3, g)
+    clean, lse = _run(q, k, v, kb, **mods)
+    _check(q, k, v, clean, lse, kb, **mods)
+    v2, k2 = v.clone(), k.clone()
+    v2[:, :, 8950:] = float("nan")           # the last view: hidden from the queries before it
+    k2[:, :, 8950:] = float("inf")
+    v2[:, :, 77, 9] = float("inf")           # seen by all, in the first part
+    out, lse2 = _run(q, k2, v2, kb, **mods)
+    before = mods["q_order"][0] < 89
+    assert bool((out[:, :, before, 9] == float("inf")).all())
+    same = torch.ones(64, dtype=torch.bool, device="cuda")
+    same[9] = False
+    assert torch.equal(out[:, :, before][..., same], clean[:, :, before][..., same])
+    assert torch.equal(lse2[:, :, before], lse[:, :, before])
+
+
+@pytest.mark.gpu
 def test_first_tile_of_a_row_holds_an_infinity():
     """The values of the first tile are added by hand before any product ran."""
     q, k, v, g = _inputs(2, 2, 260, 260, seed=5)
@@ -368,10 +390,10 @@ def test_a_block_listed_twice_counts_twice():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("Nq", [600, 2, 1])
+@pytest.mark.parametrize("Nq", [600, 300, 2, 1])
 def test_bad_lists_set_the_error_and_leave_the_row(Nq):
     """An index or a count out of range is found by the kernel's own check before any load."""
-    N = 600 if Nq == 600 else 1100                # the second in parts that are joined
+    N = {600: 600, 300: 9000}.get(Nq, 1100)       # the second in parts that are joined
     q, k, v, g = _inputs(1, 30, N, Nq)
     nq, nk = (Nq + 127) // 128, (N + 127) // 128
     shape = R.make_shape(1, 30, N)
