@@ -543,14 +543,14 @@ __global__ void __launch_bounds__(kThreads, 2)
           float big = 0.f;  // largest |score|, for the cap
           bool fused = false;
           if constexpr (CAP) {
-            float mc[4] = {0.f, 0.f, 0.f, 0.f};
+            float mc[2] = {0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < 128; c += 8) {
+            for (int c = 0; c < 128; c += 4) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
+              for (int q = 0; q < 2; ++q)
                 mc[q] = fmax3(mc[q], fabsf(__uint_as_float(sv[c + 2 * q])), fabsf(__uint_as_float(sv[c + 2 * q + 1])));
             }
-            big = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
+            big = fmaxf(mc[0], mc[1]);
             fused = !BIAS && code == kWhole && __all_sync(0xffffffffu, big <= p.cap_a);
           }
           if (code == kNone) {
@@ -970,24 +970,28 @@ __global__ void __launch_bounds__(256) no_keys_kernel(long long rows, uint4 *__r
   }
 }
 
-// CTAs that share a row: as many as keep the whole card (two per SM) busy, each with some
-// tiles of the longest possible row; long rows are split on into up to four times as many,
-// since kept lists and masks make them uneven (a part's sums cost 32 KB each way).
-constexpr int kSlots = 2 * 148, kTilesPerSplit = 8;
+// CTAs that share a row: as many as keep the whole card (two per SM) busy, each with a few
+// tiles of the longest possible row; long rows (16 tiles a part) are split on into up to four
+// times as many, since kept lists and masks make them uneven.  A part's sums cost 32 KB each
+// way and the join a dependent launch: 4 heads of 1024 tokens, causal with a prefix, 16.6 us
+// at 2 tiles a part, 17.8 at 4, 19.0 unsplit; a new view over 32 views 315 us unsplit, 204 at
+// four parts.
+constexpr int kSlots = 2 * 148, kTilesPerSplit = 2, kTilesOfUneven = 16;
 int splits_of(const Dims &d, int nq) {
   const long long items = d.BH() * nq;
   const int tiles = (int)((d.N + 127) / 128);
   if (items == 0) return 1;
   long long n = std::max(1ll, std::min(kSlots / items, (long long)(tiles / kTilesPerSplit)));
-  while (items * n * 2 <= 4 * kSlots && tiles >= 2 * n * 2 * kTilesPerSplit) n *= 2;
+  while (items * n * 2 <= 4 * kSlots && tiles >= 2 * n * kTilesOfUneven) n *= 2;
   return (int)n;
 }
 
-// Masked rows are put in order, longest first, where they come in more than one wave and
-// are long enough for the tail to matter (two small kernels, about 10 us).
+// Rows of masked calls and of kept lists are put in order, longest first, where they come in
+// more than one wave and are long enough for the tail to matter (one or two small kernels,
+// about 5 us each).
 bool plans_order(const Dims &d, int nq) {
   const long long items = d.BH() * nq;
-  return items > kSlots && items * ((d.N + 127) / 128) >= 64 * kSlots;
+  return items * splits_of(d, nq) > kSlots && items * ((d.N + 127) / 128) >= 64 * kSlots;
 }
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -1101,13 +1105,16 @@ cudaError_t launch_masked_attn(const Dims &d, const MaskedAttnLaunch &a, cudaStr
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  if (sorted && !p.order && (m.q_doc || m.q_order)) {
-    plan_kernel<<<(unsigned)((items + 7) / 8), 256, 0, st>>>(p, items, count);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+  const bool masked = m.q_doc || m.q_order;
+  if (sorted && !p.order && (masked || p.kv_cnt)) {
+    if (masked) {
+      plan_kernel<<<(unsigned)((items + 7) / 8), 256, 0, st>>>(p, items, count);
+      cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
     Dims rows = d;
     rows.nb = rows.nq = nq;
-    e = launch_schedule(rows, count, sorted, st);
+    cudaError_t e = launch_schedule(rows, masked ? count : p.kv_cnt, sorted, st);
     if (e != cudaSuccess) return e;
     p.order = sorted;
   }
@@ -1117,7 +1124,7 @@ cudaError_t launch_masked_attn(const Dims &d, const MaskedAttnLaunch &a, cudaStr
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   e = launch_after(kern, dim3((unsigned)items, (unsigned)p.splits), kThreads, kSmemBytes, st,
-                   m.q_doc || m.q_order || m.slopes, mq, mk, mv, p);
+                   masked || m.slopes || (sorted && p.order == sorted), mq, mk, mv, p);
   if (e != cudaSuccess || p.splits == 1) return e;
   return launch_after(join_kernel, dim3((unsigned)((rows + 7) / 8)), 256, 0, st, true, (const float *)p.part_o,
                       (const float2 *)p.part_ml, p.splits, nq, Nq, rows, p.out, p.lse);
