@@ -104,11 +104,14 @@ RESS_DEV void cap_small(uint32_t (&sv)[128], float in) {
     sv[c + 1] = __float_as_uint(f2hi(u));
   }
 }
-// Any score.
+// Any score: 1 - 2 / (1 + e^2y), off by an fp32 unit absolutely, which is all that the
+// exponent takes from it.
 RESS_DEV void cap_any(uint32_t (&sv)[128], float in) {
+  const float in2 = 2.0f * kLog2e * in;
 #pragma unroll
   for (int c = 0; c < 128; ++c) {
-    sv[c] = __float_as_uint(tanh_any(__uint_as_float(sv[c]) * in));
+    const float r = rcp_approx(1.0f + ex2_approx(__uint_as_float(sv[c]) * in2));
+    sv[c] = __float_as_uint(fmaf(-2.0f, r, 1.0f));
   }
 }
 
@@ -135,7 +138,7 @@ struct Params {
   float scale_log2;         // without a cap
   float cap_log2, cap_in;   // c log2 e; scale / c
   float cap_half;           // scores up to this stay within |y| = 1/2
-  float cap_a, cap_k[4];    // and up to this (|y| = 3/8) the cap is s cap_k(s^2), log2 domain
+  float cap_a, cap_k[4];    // and up to this (|y| = 3/8, |z| = 32) the cap is s cap_k(s^2), log2 domain
 };
 
 // KB tokens per key block; CAP, BIAS: the score changes compiled in.
@@ -518,13 +521,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           uint32_t pk[64];
           // P and its sum from the exponents of column pairs
           auto weights = [&](auto z_of) {
-            alpha = rescale ? ex2_approx(m_run - m_use) : 1.0f;
-            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+            constexpr int kChains = CAP ? 2 : 4;  // sums; the cap leaves fewer registers
+            uint64_t acc[kChains] = {};
 #pragma unroll
             for (int c = 0; c < 64; ++c) {
               const uint64_t z = z_of(c);
               const uint64_t e = f2(ex2_approx(f2lo(z)), ex2_approx(f2hi(z)));
-              acc[c & 3] = fadd2(acc[c & 3], e);
+              acc[c % kChains] = fadd2(acc[c % kChains], e);
               pk[c] = pack_bf16x2(f2lo(e), f2hi(e));
               if (c == 31) {
                 // keys 0..63 of P: free once the first half of the previous product is done
@@ -532,7 +535,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 tmem_st32(trow + kColP, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
               }
             }
-            const uint64_t a = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+            uint64_t a = fadd2(acc[0], acc[1]);
+            if (kChains == 4) a = fadd2(a, fadd2(acc[kChains - 2], acc[kChains - 1]));
+            alpha = rescale ? ex2_approx(m_run - m_use) : 1.0f;
             l_run = l_run * alpha + (f2lo(a) + f2hi(a));
             m_run = m_use;
           };
@@ -1075,10 +1080,10 @@ cudaError_t launch_masked_attn(const Dims &d, const MaskedAttnLaunch &a, cudaStr
   p.cap_in = m.softcap > 0.f ? a.scale / m.softcap : 0.f;
   p.cap_half = 0.5f / p.cap_in;
   // The fused cap: its coefficients must keep their range, and the bound that it takes for
-  // the row's maximum may lie 2 tanh(3/8) C above it, which costs exponents that range.
+  // the row's maximum may lie 2 |z| above it, which costs the exponents that range: 64 at most.
   p.cap_a = -1.f;
-  if (p.cap_in > 1e-5f && p.cap_in < 1e5f && 0.72f * p.cap_log2 <= 64.f) {
-    p.cap_a = 0.375f / p.cap_in;
+  if (p.cap_in > 1e-5f && p.cap_in < 1e5f) {
+    p.cap_a = std::min(0.375f / p.cap_in, 32.f / p.scale_log2);
     double k = (double)p.cap_log2 * p.cap_in;
     for (int i = 0; i < 4; ++i, k *= (double)p.cap_in * p.cap_in) p.cap_k[i] = (float)(kTanhFit3[i] * k);
   }
