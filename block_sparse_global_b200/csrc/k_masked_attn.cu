@@ -160,6 +160,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (p.order) wait_prerequisites();  // (an order of our own is written by the kernel before)
   const int x = blockIdx.x;
   const int item32 = p.order ? p.order[x] : x / p.nq * p.nq + (p.nq - 1 - x % p.nq);
+  if (p.order && (item32 < 0 || item32 >= (int)gridDim.x)) {  // not a permutation
+    if (tid == 0) report_error(p.dev_err, RESS_ERR_DEVICE_BOUNDS);
+    return;
+  }
   const int bh = item32 / p.nq, qi = item32 - bh * p.nq, b = bh / p.H;
   const long long item = item32;
   const bool masked = p.q_doc != nullptr || p.q_order != nullptr;
@@ -1055,7 +1059,6 @@ cudaError_t launch_masked_attn(const Dims &d, const MaskedAttnLaunch &a, cudaStr
   Params p = {};
   p.kv_idx = a.kv_idx;
   p.kv_cnt = a.kv_cnt;
-  p.order = a.order;
   if (m.slopes) {
     p.slopes = m.slopes;
     p.q_pos = m.q_pos;
@@ -1075,6 +1078,9 @@ cudaError_t launch_masked_attn(const Dims &d, const MaskedAttnLaunch &a, cudaStr
   p.nq = nq;
   p.nk = d.nk;
   p.splits = splits_of(d, nq);
+  // rows in parts are few, or put in order below; a caller's order that left one out would
+  // leave its parts unwritten for the join
+  p.order = p.splits == 1 ? a.order : nullptr;
   p.scale_log2 = a.scale * kLog2e;
   p.cap_log2 = m.softcap * kLog2e;
   p.cap_in = m.softcap > 0.f ? a.scale / m.softcap : 0.f;

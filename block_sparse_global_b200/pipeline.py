@@ -50,6 +50,8 @@ class SparseGlobalAttention:
         self.dev_err = torch.zeros(4, **i32)
         self.gram = torch.empty(H, 64, 64, **f32)
         self.scale = 1.0 / math.sqrt(64)
+        self._qkv = None      # prepare()'s outputs
+        self._masked_ws = {}  # attend_masked()'s workspaces
 
     def load_output_projection(self, w_o: torch.Tensor, stream=None):
         """M_h = W_O^h^T W_O^h for every head (ReSS Eq. 8), computed once per layer."""
@@ -62,7 +64,7 @@ class SparseGlobalAttention:
         per-head norm and the rotary positions of q and k, and the move of every view's
         special tokens to the tail, in one pass.  The three tensors belong to the layer and
         are overwritten by the next call."""
-        if getattr(self, "_qkv", None) is None:
+        if self._qkv is None:
             self._qkv = [torch.empty(self.B, self.H, self.N, 64, device=self.device,
                                      dtype=torch.bfloat16) for _ in range(3)]
         if packed.shape != (self.B, self.N, 3, self.H, 64):
@@ -135,13 +137,14 @@ class SparseGlobalAttention:
                                  self.order if schedule else None, self.scale, self.out, self.lse,
                                  self.dev_err, stream)
 
-    def attend_masked(self, q, k, v, kept: bool = True, out=None, lse=None, schedule: bool = True,
-                      stream=None, **mods):
+    def attend_masked(self, q, k, v, kept: bool = True, out=None, lse=None, stream=None, **mods):
         """Attention with changed scores (`mods`: softcap, slopes, q_/k_ pos, doc and order, as
         for ress_masked_attn) of q [B,H,q_len,64] over this layer's k, v.  kept: over the
         selected blocks, for all of the sequence's tokens (q_len = N); otherwise over every
         block, for any q_len (new tokens over a cache).  Without `out`, the result goes to
-        the layer's out and lse if q_len = N, else to a new tensor."""
+        the layer's out and lse if q_len = N, else to a new tensor.  The layer keeps one
+        workspace per number of query blocks, for eager calls and captured graphs alike:
+        such calls of one layer must not overlap in time."""
         n = q.shape[2]
         if kept and n != self.N:
             raise ValueError("the kept blocks are those of the sequence's own tokens")
@@ -150,16 +153,15 @@ class SparseGlobalAttention:
                 out, lse = self.out, self.lse if lse is None else lse
             else:
                 out = torch.empty(self.B, self.H, n, 64, device=self.device, dtype=torch.bfloat16)
-        need = R.ress_masked_attn_workspace_bytes(self.shape, n)
-        ws = getattr(self, "_masked_ws", None)
-        if ws is None or ws.numel() < need:
-            ws = self._masked_ws = torch.empty(need, device=self.device, dtype=torch.uint8)
-        if kept and schedule:
-            R.ress_attn_schedule(self.shape, self.kv_cnt, self.order, stream)
+        # kept for good: a captured graph holds its address
+        ws = self._masked_ws.get((n + 127) // 128)
+        if ws is None:
+            need = R.ress_masked_attn_workspace_bytes(self.shape, (n + 127) // 128 * 128)
+            ws = torch.empty(max(need, 16), device=self.device, dtype=torch.uint8)
+            self._masked_ws[(n + 127) // 128] = ws
         R.ress_masked_attn(self.shape, q, k, v, self.kv_idx if kept else None,
-                           self.kv_cnt if kept else None, self.order if kept and schedule else None,
-                           self.scale, out, lse, workspace=ws, dev_err=self.dev_err[:1],
-                           stream=stream, **mods)
+                           self.kv_cnt if kept else None, None, self.scale, out, lse, workspace=ws,
+                           dev_err=self.dev_err[:1], stream=stream, **mods)
         return out
 
     def forward(self, q, k, v, method: int, budgets: Sequence[int], keep_k=None, dense_q=None,

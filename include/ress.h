@@ -561,7 +561,9 @@ size_t ress_masked_attn_workspace_bytes(const ress_shape *shape, int32_t q_len);
  *   kv_idx   int32 [B,H,nq,nk] and kv_cnt int32 [B,H,nq], as for ress_block_sparse_attn; or
  *            both NULL: every key block is kept.  Blocks that no query of a row sees are
  *            passed over unread.  A block listed twice counts twice.
- *   work_order int32 [B*H*nq] permutation or NULL.  Outputs do not depend on it.
+ *   work_order int32 [B*H*nq] permutation or NULL: an order of the library's own (rows that
+ *            see most first, where that pays).  Outputs do not depend on it.  Calls of few
+ *            rows do not look at it; otherwise an entry out of range is reported by dev_err.
  *   mods     HOST; NULL: q_len = N and scores as they are.
  *   workspace  DEVICE scratch of at least ress_masked_attn_workspace_bytes(shape, q_len)
  *            bytes, 16-byte aligned, overwritten; calls that may overlap in time need one

@@ -434,7 +434,7 @@ def test_guards_streams_and_graphs_with_their_own_workspaces():
     """Two calls at once on two streams, captured and replayed on new data; memory around the
     outputs stays."""
     sets = []
-    for i, (N, Nq) in enumerate(((3000, 2), (777, 777))):
+    for i, (N, Nq) in enumerate(((3000, 2), (777, 777), (9000, 200))):
         q, k, v, g = _inputs(1, 3, N, Nq, seed=20 + i)
         mods = _arrays(1, N, Nq, 2, 9, "token", 0.0, 3, g)
         room = torch.full((3 * Nq * 64 + 128,), 5.0, dtype=BF16, device="cuda")
@@ -500,3 +500,35 @@ def test_layer_with_masks_from_projection_to_new_tokens(key_block):
     _check(turned, k, v, got, lse, key_block, **step)
     with pytest.raises(ValueError):
         layer.attend_masked(turned, k, v)
+
+
+@pytest.mark.gpu
+def test_order_that_is_no_permutation_sets_the_error():
+    """An entry of work_order out of range is found by the kernel's own check."""
+    q, k, v, g = _inputs(1, 40, 500, 500)       # 160 rows: one CTA each
+    order = torch.arange(160, dtype=torch.int32, device="cuda")
+    want, _ = _run(q, k, v)
+    order[3], order[5] = 160, -1
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, _ = _run(q, k, v, order=order, dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err) == 4
+    assert bool((out[0, 0, 384:] == 3).all()) and bool((out[0, 1, 128:256] == 3).all())
+    assert torch.equal(out[0, 2:], want[0, 2:]) and torch.equal(out[0, 0, :384], want[0, 0, :384])
+
+
+@pytest.mark.gpu
+def test_layer_graph_of_new_tokens_outlives_larger_calls():
+    """A captured call keeps its workspace when later calls of the layer need larger ones."""
+    layer = SparseGlobalAttention(1, 4, 9000)
+    q, k, v, g = _inputs(1, 4, 9000, 200, seed=30)
+    out = torch.empty(1, 4, 200, 64, dtype=BF16, device="cuda")
+    graph = layer.capture(lambda: layer.attend_masked(q, k, v, kept=False, out=out, softcap=20.0))
+    big = torch.randn(1, 4, 2000, 64, device="cuda").to(BF16)
+    layer.attend_masked(big, k, v, kept=False)
+    junk = [torch.full((1 << 22,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    q.copy_(-q)
+    graph.replay()
+    torch.cuda.synchronize()
+    want, _ = _run(q, k, v, softcap=20.0)
+    assert torch.equal(out, want) and len(junk) == 8
