@@ -74,7 +74,7 @@ struct TokenParams {
   int views, specials, view_tokens;  // view_tokens = 0: rows keep their places
   int groups;                        // element form: warps that share a token's heads
   long long tasks;                   // element form: B * N * groups
-  int tile, tiles;                   // 16-byte form: tokens of a CTA, CTAs of a batch entry
+  int tile, tiles;                   // chunk form: tokens of a CTA, CTAs of a batch entry
   uint64_t phase[kMaxPairs];         // turns per position of each pair of a section
 };
 
@@ -122,10 +122,11 @@ RESS_DEV float row_sum(float v, int lanes) {
   return v;
 }
 
-// ------------------------------------------------------------------- 16-byte form
-// A lane holds two 16-byte chunks of a row, so that a rotated pair never leaves the lane:
-// chunks half a section apart in the half layout, neighbours in the interleaved one.  A row
-// takes D / 2V lanes, rounded up to a power of two (the rest idle), and a warp's pass several
+// ------------------------------------------------------------------- chunk form
+// A lane holds two chunks of V elements of a row, so that a rotated pair never leaves the
+// lane: chunks half a section apart in the half layout, neighbours in the interleaved one.
+// Chunks are of 16 bytes, or of 8 or 4 where sections, strides or addresses allow no more
+// (half a section of 20 elements: 8 bytes of a 16-bit type).  A row takes D / 2V lanes, rounded up to a power of two (the rest idle), and a warp's pass several
 // heads of one token.  The passes of all tensors and the CTA's tokens form one list, pass by
 // pass, of which each warp takes an equal stretch: a few runs of tokens of one pass, in which
 // pointers advance, weights and biases stay in registers and kPieces tokens' loads are in
@@ -159,56 +160,59 @@ RESS_DEV uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// 16 bytes as pairs of fp32, and back with one rounding.
-template <typename T>
-RESS_DEV void unpack(const uint4 &raw, uint64_t *x);
-template <>
-RESS_DEV void unpack<float>(const uint4 &raw, uint64_t *x) {
-  x[0] = ((uint64_t)raw.y << 32) | raw.x;
-  x[1] = ((uint64_t)raw.w << 32) | raw.z;
-}
-template <>
-RESS_DEV void unpack<__nv_bfloat16>(const uint4 &raw, uint64_t *x) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+// A chunk of V elements as it lies in memory, as V / 2 pairs of fp32, and back with one
+// rounding.
+template <typename T, int V>
+struct alignas(V * sizeof(T)) Chunk {
+  uint32_t w[V * sizeof(T) / 4];
+};
+template <int V>
+RESS_DEV void unpack(const Chunk<float, V> &raw, uint64_t *x) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = ((uint64_t)(w[i] & 0xffff0000u) << 32) | (w[i] << 16);
+  for (int i = 0; i < V / 2; ++i) x[i] = ((uint64_t)raw.w[2 * i + 1] << 32) | raw.w[2 * i];
 }
-template <>
-RESS_DEV void unpack<__half>(const uint4 &raw, uint64_t *x) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+template <int V>
+RESS_DEV void unpack(const Chunk<__nv_bfloat16, V> &raw, uint64_t *x) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+  for (int i = 0; i < V / 2; ++i) x[i] = ((uint64_t)(raw.w[i] & 0xffff0000u) << 32) | (raw.w[i] << 16);
+}
+template <int V>
+RESS_DEV void unpack(const Chunk<__half, V> &raw, uint64_t *x) {
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&raw.w[i]));
     x[i] = pk2(v.x, v.y);
   }
 }
-template <typename T>
-RESS_DEV uint4 repack(const uint64_t *x);
-template <>
-RESS_DEV uint4 repack<float>(const uint64_t *x) {
-  return make_uint4((uint32_t)x[0], (uint32_t)(x[0] >> 32), (uint32_t)x[1], (uint32_t)(x[1] >> 32));
-}
-template <>
-RESS_DEV uint4 repack<__nv_bfloat16>(const uint64_t *x) {
-  return make_uint4(pack_bf16x2(lo2(x[0]), hi2(x[0])), pack_bf16x2(lo2(x[1]), hi2(x[1])),
-                    pack_bf16x2(lo2(x[2]), hi2(x[2])), pack_bf16x2(lo2(x[3]), hi2(x[3])));
-}
-template <>
-RESS_DEV uint4 repack<__half>(const uint64_t *x) {
-  uint32_t w[4];
+template <int V>
+RESS_DEV void repack(const uint64_t *x, Chunk<float, V> &raw) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = __floats2half2_rn(lo2(x[i]), hi2(x[i]));
-    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  for (int i = 0; i < V / 2; ++i) {
+    raw.w[2 * i] = (uint32_t)x[i];
+    raw.w[2 * i + 1] = (uint32_t)(x[i] >> 32);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int V>
+RESS_DEV void repack(const uint64_t *x, Chunk<__nv_bfloat16, V> &raw) {
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) raw.w[i] = pack_bf16x2(lo2(x[i]), hi2(x[i]));
+}
+template <int V>
+RESS_DEV void repack(const uint64_t *x, Chunk<__half, V> &raw) {
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    const __half2 h = __floats2half2_rn(lo2(x[i]), hi2(x[i]));
+    raw.w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
 }
 
-// HALF: the pair layout; NORM: ress_norm.
-template <typename T, bool HALF, int NORM>
+// HALF: the pair layout; NORM: ress_norm, or kAnyNorm (the narrow chunks: fewer kernels).
+constexpr int kAnyNorm = -1;
+template <typename T, int V, bool HALF, int NORM>
 __global__ void __launch_bounds__(kThreads, NORM == RESS_NORM_NONE ? kCtasRotate : kCtasNorm)
-    token_vec_kernel(const __grid_constant__ TokenParams p) {
-  constexpr int V = 16 / sizeof(T);  // elements of a chunk
+    token_chunk_kernel(const __grid_constant__ TokenParams p) {
+  using Raw = Chunk<T, V>;
+  const int norm = NORM == kAnyNorm ? p.norm : NORM;
   __shared__ __align__(16) float cs[kAngleFloats];
   __shared__ __align__(16) float wb[4][kMaxDim];
   __shared__ int to[kMaxTile];  // rows that the tokens go to
@@ -240,15 +244,15 @@ __global__ void __launch_bounds__(kThreads, NORM == RESS_NORM_NONE ? kCtasRotate
   bool there = false;
   const T *src = nullptr;
   T *dst = nullptr;
-  uint4 next[kPieces][2];
+  Raw next[kPieces][2];
   auto load = [&](int t) {
     const long long in_t = p.part[which].in_t;
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
-      next[u][0] = next[u][1] = make_uint4(0, 0, 0, 0);
+      next[u][0] = next[u][1] = Raw{};
       if (there && t + u < tb) {
-        next[u][0] = *reinterpret_cast<const uint4 *>(src + ca);
-        next[u][1] = *reinterpret_cast<const uint4 *>(src + cb);
+        next[u][0] = *reinterpret_cast<const Raw *>(src + ca);
+        next[u][1] = *reinterpret_cast<const Raw *>(src + cb);
       }
       src += in_t;
     }
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, NORM == RESS_NORM_NONE ? kCtasRotate
     }
   }
   if (tid < nt) to[tid] = target_row(p, t0 + tid);
-  if (NORM != RESS_NORM_NONE) {
+  if (norm != RESS_NORM_NONE) {
     for (int i = tid; i < p.D; i += kThreads) {
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
@@ -291,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, NORM == RESS_NORM_NONE ? kCtasRotate
     const long long out_t = p.part[which].out_t;
     const bool work = p.part[which].work;
     uint64_t w[V], bias[V];  // V / 2 pairs of chunk a, then of chunk b
-    if (NORM != RESS_NORM_NONE && work) {
+    if (norm != RESS_NORM_NONE && work) {
       const int ra = holds ? ca : 0, rb = holds ? cb : 0;
 #pragma unroll
       for (int e = 0; e < V / 2; ++e) {
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, NORM == RESS_NORM_NONE ? kCtasRotate
       }
     }
     for (int t = ta; t < tb; t += kPieces) {
-      uint4 raw[kPieces][2];
+      Raw raw[kPieces][2];
 #pragma unroll
       for (int u = 0; u < kPieces; ++u) {
         raw[u][0] = next[u][0];
@@ -314,10 +318,10 @@ __global__ void __launch_bounds__(kThreads, NORM == RESS_NORM_NONE ? kCtasRotate
         if (t + u >= tb) break;
         if (work) {
           uint64_t x[V];
-          unpack<T>(raw[u][0], x);
-          unpack<T>(raw[u][1], x + V / 2);
-          if (NORM != RESS_NORM_NONE) {
-            if (NORM == RESS_NORM_LAYER) {
+          unpack(raw[u][0], x);
+          unpack(raw[u][1], x + V / 2);
+          if (norm != RESS_NORM_NONE) {
+            if (norm == RESS_NORM_LAYER) {
               uint64_t m = x[0];
 #pragma unroll
               for (int e = 1; e < V; ++e) m = add2(m, x[e]);
@@ -339,10 +343,16 @@ __global__ void __launch_bounds__(kThreads, NORM == RESS_NORM_NONE ? kCtasRotate
             const float *c = cs + 2 * slots * (t + u) + own * V, *s = c + slots;
 #pragma unroll
             for (int e = 0; e < V / 2; e += 2) {
-              const ulonglong2 ce2 = *reinterpret_cast<const ulonglong2 *>(c + 2 * e);
-              const ulonglong2 se2 = *reinterpret_cast<const ulonglong2 *>(s + 2 * e);
+              ulonglong2 ce2, se2;
+              if constexpr (V >= 4) {
+                ce2 = *reinterpret_cast<const ulonglong2 *>(c + 2 * e);
+                se2 = *reinterpret_cast<const ulonglong2 *>(s + 2 * e);
+              } else {
+                ce2.x = *reinterpret_cast<const uint64_t *>(c);
+                se2.x = *reinterpret_cast<const uint64_t *>(s);
+              }
 #pragma unroll
-              for (int f = 0; f < 2; ++f) {
+              for (int f = 0; f < (V >= 4 ? 2 : 1); ++f) {
                 const uint64_t ce = f ? ce2.y : ce2.x, se = f ? se2.y : se2.x;
                 if (HALF) {  // pairs (x_a, x_b)
                   const uint64_t ns = se ^ 0x8000000080000000ull;
@@ -361,13 +371,13 @@ __global__ void __launch_bounds__(kThreads, NORM == RESS_NORM_NONE ? kCtasRotate
               }
             }
           }
-          raw[u][0] = repack<T>(x);
-          raw[u][1] = repack<T>(x + V / 2);
+          repack(x, raw[u][0]);
+          repack(x + V / 2, raw[u][1]);
         }
         if (there) {
           T *row = dst + to[t + u] * out_t;
-          *reinterpret_cast<uint4 *>(row + ca) = raw[u][0];
-          *reinterpret_cast<uint4 *>(row + cb) = raw[u][1];
+          *reinterpret_cast<Raw *>(row + ca) = raw[u][0];
+          *reinterpret_cast<Raw *>(row + cb) = raw[u][1];
         }
       }
     }
@@ -376,8 +386,9 @@ __global__ void __launch_bounds__(kThreads, NORM == RESS_NORM_NONE ? kCtasRotate
 }
 
 // ------------------------------------------------------------------- element form
-// Any head size up to 256, any strides, any even split of the rotated part: a warp takes
-// the rows of a token one after another, elements spread over its lanes.
+// What the chunk form leaves: odd head sizes and addresses, and sections of wide heads that
+// only single elements halve.  A warp takes the rows of a token one after another, elements
+// spread over its lanes.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) token_elem_kernel(const __grid_constant__ TokenParams p) {
   constexpr int R = kMaxDim / 32;
@@ -476,47 +487,56 @@ __global__ void __launch_bounds__(kThreads) token_elem_kernel(const __grid_const
 
 bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
-template <typename T, bool HALF>
-void launch_vec(const TokenParams &p, unsigned ctas, cudaStream_t st) {
-  if (p.norm == RESS_NORM_NONE)
-    token_vec_kernel<T, HALF, RESS_NORM_NONE><<<ctas, kThreads, 0, st>>>(p);
+template <typename T, int V, bool HALF>
+void launch_chunks(const TokenParams &p, unsigned ctas, cudaStream_t st) {
+  if constexpr (V * sizeof(T) < 16)
+    token_chunk_kernel<T, V, HALF, kAnyNorm><<<ctas, kThreads, 0, st>>>(p);
+  else if (p.norm == RESS_NORM_NONE)
+    token_chunk_kernel<T, V, HALF, RESS_NORM_NONE><<<ctas, kThreads, 0, st>>>(p);
   else if (p.norm == RESS_NORM_RMS)
-    token_vec_kernel<T, HALF, RESS_NORM_RMS><<<ctas, kThreads, 0, st>>>(p);
+    token_chunk_kernel<T, V, HALF, RESS_NORM_RMS><<<ctas, kThreads, 0, st>>>(p);
   else
-    token_vec_kernel<T, HALF, RESS_NORM_LAYER><<<ctas, kThreads, 0, st>>>(p);
+    token_chunk_kernel<T, V, HALF, RESS_NORM_LAYER><<<ctas, kThreads, 0, st>>>(p);
 }
 
 template <typename T>
 cudaError_t launch_typed(TokenParams &p, int sms, cudaStream_t st) {
-  constexpr int V = 16 / (int)sizeof(T);
-  // the 16-byte form: rows are whole pairs of chunks on 16-byte boundaries, and the pairs of
-  // the half layout lie whole chunks apart
+  // the widest chunks whose pairs make up a row in at most 32 lanes, lie on their boundaries
+  // in every tensor, and (half layout) halve a section
   const bool half = p.layout == RESS_ROPE_HALF;
-  bool vec = p.D % (2 * V) == 0;
-  if (p.rot > 0 && half) vec = vec && (p.rot / p.axes) % (2 * V) == 0;
-  int rows = 0;
-  for (int i = 0; i < p.parts; ++i) {
-    const Part &q = p.part[i];
-    vec = vec && aligned(q.in, 16) && aligned(q.out, 16);
-    for (long long s : {q.in_b, q.in_h, q.in_t, q.out_b, q.out_h, q.out_t}) vec = vec && s % V == 0;
-    rows += q.heads;
+  int V = 16 / (int)sizeof(T);
+  for (; V >= 2; V /= 2) {
+    bool fits = V * sizeof(T) >= 4 && p.D % (2 * V) == 0 && p.D / (2 * V) <= 32;
+    if (p.rot > 0 && half) fits = fits && (p.rot / p.axes) % (2 * V) == 0;
+    for (int i = 0; i < p.parts; ++i) {
+      const Part &q = p.part[i];
+      fits = fits && aligned(q.in, V * sizeof(T)) && aligned(q.out, V * sizeof(T));
+      for (long long s : {q.in_b, q.in_h, q.in_t, q.out_b, q.out_h, q.out_t}) fits = fits && s % V == 0;
+    }
+    if (fits) break;
   }
   const long long tokens = (long long)p.B * p.N;
-  if (vec) {
+  if (V >= 2) {
     // full waves of resident CTAs, of as many tokens as their angles have room for
     const long long most = kAngleFloats / p.D < kMaxTile ? kAngleFloats / p.D : kMaxTile;
-    const long long wave = (long long)sms * (p.norm == RESS_NORM_NONE ? kCtasRotate : kCtasNorm);
+    const bool lean = p.norm == RESS_NORM_NONE && V * sizeof(T) == 16;
+    const long long wave = (long long)sms * (lean ? kCtasRotate : kCtasNorm);
     const long long waves = (tokens + most * wave - 1) / (most * wave);
     const long long tile = (tokens + waves * wave - 1) / (waves * wave);
     p.tile = (int)(tile < p.N ? tile : p.N);
     p.tiles = (p.N + p.tile - 1) / p.tile;
     const unsigned ctas = (unsigned)((long long)p.tiles * p.B);
-    if (half)
-      launch_vec<T, true>(p, ctas, st);
-    else
-      launch_vec<T, false>(p, ctas, st);
+    constexpr int W = 16 / sizeof(T);
+    if (V == W)
+      half ? launch_chunks<T, W, true>(p, ctas, st) : launch_chunks<T, W, false>(p, ctas, st);
+    else if (V == W / 2)
+      half ? launch_chunks<T, W / 2, true>(p, ctas, st) : launch_chunks<T, W / 2, false>(p, ctas, st);
+    else if constexpr (W == 8)
+      half ? launch_chunks<T, 2, true>(p, ctas, st) : launch_chunks<T, 2, false>(p, ctas, st);
     return cudaGetLastError();
   }
+  int rows = 0;
+  for (int i = 0; i < p.parts; ++i) rows += p.part[i].heads;
   // few tokens: spread a token's heads over warps until the card has some for every
   // scheduler; each then computes the token's angles again
   const long long want = (long long)sms * 16;

@@ -199,7 +199,9 @@ ROPE_CASES = [  # dim, rot, axes, layout, dtype, B, H, N
     (256, 256, 2, "half", FP32, 1, 2, 20), (256, 128, 1, "half", BF16, 1, 3, 65),
     (32, 2, 1, "half", BF16, 1, 7, 19), (64, 10, 1, "interleaved", FP16, 1, 3, 19), (2, 2, 1, "half", FP32, 1, 2, 9),
     (33, 32, 2, "interleaved", BF16, 2, 2, 50), (254, 252, 3, "half", FP16, 1, 1, 8),
-    (64, 64, 2, "half", BF16, 1, 2, 20011), (72, 40, 1, "half", FP16, 1, 1, 70001)]
+    (64, 64, 2, "half", BF16, 1, 2, 20011), (72, 40, 1, "half", FP16, 1, 1, 70001),
+    (64, 20, 1, "half", FP32, 2, 3, 33), (64, 36, 1, "half", BF16, 2, 3, 33), (68, 68, 1, "interleaved", FP16, 1, 2, 9),
+    (128, 72, 3, "half", FP32, 1, 2, 11)]
 
 
 @pytest.mark.gpu
@@ -330,7 +332,10 @@ QK_CASES = [  # dim, rot, axes, layout, dtype, B, H, G, N, norm, affine, with_v,
     (31, 30, 3, "half", BF16, 1, 3, 1, 21, "layer", True, True, 7, 2),
     (64, 0, 1, "half", BF16, 2, 3, 3, 50, "rms", True, True, 1, 0),
     (64, 64, 1, "half", BF16, 1, 12, 12, 30, "none", False, True, 5, 1),
-    (32, 32, 1, "interleaved", FP16, 1, 1, 1, 40011, "rms", True, True, 1, 0)]
+    (32, 32, 1, "interleaved", FP16, 1, 1, 1, 40011, "rms", True, True, 1, 0),
+    (64, 36, 1, "half", BF16, 2, 5, 1, 66, "layer", True, True, 3, 2),
+    (72, 24, 3, "half", FP16, 1, 3, 3, 21, "none", False, True, 1, 0),
+    (80, 20, 1, "half", FP32, 1, 4, 2, 19, "rms", True, True, 1, 0)]
 
 
 @pytest.mark.gpu
