@@ -208,6 +208,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 
   // ---------------------------------------------------------------- the row's blocks
+  // the loads of this thread's first entry go out before the queries' arrays are looked at
+  wait_prerequisites();  // the summaries
+  const int cnt = p.kv_cnt ? p.kv_cnt[item] : p.nk;
+  const int32_t *kvrow = p.kv_idx ? p.kv_idx + item * p.nk : nullptr;
+  const int kb0 = kvrow ? (tid < p.nk ? kvrow[tid] : -1) : tid;  // (past cnt: anything)
+  int4 sum0 = make_int4(0, 0, 0, 0);
+  if (masked && kb0 >= 0 && kb0 < p.nk) sum0 = p.blocks[(long long)b * p.nk + kb0];
   const int t = qi * 128 + tid;  // query token of a softmax thread
   if (warp < 4) {
     int row_doc = 0, row_order = 0;
@@ -227,9 +234,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < 5; ++i) bar->qsum[warp][i] = v[i];
   }
   __syncthreads();
-  wait_prerequisites();  // the summaries
-  const int cnt = p.kv_cnt ? p.kv_cnt[item] : p.nk;
-  const int32_t *kvrow = p.kv_idx ? p.kv_idx + item * p.nk : nullptr;
   const bool ragged = p.N % KB != 0;
   bool bad = cnt < 0 || cnt > p.nk;
   int kept = 0;
@@ -240,12 +244,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       bool see = false;
       uint32_t cls = 0;
       if (j < cnt) {
-        kb = kvrow ? kvrow[j] : j;
+        kb = j0 == 0 ? kb0 : (kvrow ? kvrow[j] : j);
         if (kb < 0 || kb >= p.nk) {
           bad = true;
         } else {
-          int4 sum = make_int4(0, 0, 0, 0);
-          if (masked) sum = p.blocks[(long long)b * p.nk + kb];
+          int4 sum = sum0;
+          if (masked && j0 > 0) sum = p.blocks[(long long)b * p.nk + kb];
           const bool cut = ragged && kb == p.nk - 1;
           for (int w = 0; w < active; ++w) {
             bool some = true, whole = !cut;
