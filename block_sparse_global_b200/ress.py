@@ -67,7 +67,7 @@ class ress_qk_params(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("norm", ctypes.c_int32), ("eps", ctypes.c_float),
                 ("q_weight", ctypes.c_void_p), ("q_bias", ctypes.c_void_p),
                 ("k_weight", ctypes.c_void_p), ("k_bias", ctypes.c_void_p),
-                ("rope", ctypes.POINTER(ress_rope_plan)), ("positions", ctypes.c_void_p),
+                ("rope", ctypes.c_void_p), ("positions", ctypes.c_void_p),
                 ("pos_stride_b", ctypes.c_int64), ("views", ctypes.c_int32),
                 ("specials", ctypes.c_int32)]
 
@@ -427,7 +427,7 @@ def ress_qk_norm_rope(q, k, q_out, k_out, v=None, v_out=None, norm: int = NORM_R
     pos, pos_b = (None, 0) if plan is None else _positions(plan, positions, b, n, dev)
     p = ress_qk_params(b, n, h, kv[1], d, DTYPES[dtype], norm, eps, _affine(q_weight, d, dev),
                        _affine(q_bias, d, dev), _affine(k_weight, d, dev), _affine(k_bias, d, dev),
-                       None if plan is None else ctypes.pointer(plan), pos, pos_b, views, specials)
+                       None if plan is None else ctypes.addressof(plan), pos, pos_b, views, specials)
     _launch("ress_qk_norm_rope", dev, stream, p, _rows(q, shape, dtype, dev),
             _rows(k, kv, dtype, dev), None if v is None else _rows(v, kv, dtype, dev),
             _rows(q_out, shape, dtype, dev), _rows(k_out, kv, dtype, dev),
@@ -446,7 +446,9 @@ def _sized(t: Optional[torch.Tensor], shape, dtype, device, name: str):
     if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
-    return _ptr(t)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr() or None
 
 
 def ress_masked_attn(shape, q, k, v, kv_idx, kv_cnt, work_order, scale: float, out, lse=None,
@@ -464,22 +466,31 @@ def ress_masked_attn(shape, q, k, v, kv_idx, kv_cnt, work_order, scale: float, o
     nq, nk = grid(n)[0], grid(N, s.key_block)[1]
     bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
     qd, kd = (B, n), (B, N)
-    m = ress_attn_mods(n, float(softcap), _sized(slopes, (H,), f32, dev, "slopes"),
-                       _sized(q_pos, qd, i32, dev, "q_pos"), _sized(k_pos, kd, i32, dev, "k_pos"),
-                       _sized(q_doc, qd, i32, dev, "q_doc"), _sized(k_doc, kd, i32, dev, "k_doc"),
-                       _sized(q_order, qd, i32, dev, "q_order"),
-                       _sized(k_order, kd, i32, dev, "k_order"))
+    m = ress_attn_mods(n, softcap)
+    if slopes is not None:
+        m.slopes = _sized(slopes, (H,), f32, dev, "slopes")
+    if q_pos is not None or k_pos is not None:
+        m.q_pos, m.k_pos = _sized(q_pos, qd, i32, dev, "q_pos"), _sized(k_pos, kd, i32, dev, "k_pos")
+    if q_doc is not None or k_doc is not None:
+        m.q_doc, m.k_doc = _sized(q_doc, qd, i32, dev, "q_doc"), _sized(k_doc, kd, i32, dev, "k_doc")
+    if q_order is not None or k_order is not None:
+        m.q_order = _sized(q_order, qd, i32, dev, "q_order")
+        m.k_order = _sized(k_order, kd, i32, dev, "k_order")
     nbytes = 0
     if workspace is not None:
         if workspace.device != dev:
             raise ValueError("the workspace is on another device")
         nbytes = workspace.numel() * workspace.element_size()
-    if work_order is not None and work_order.numel() != B * H * nq:
-        raise ValueError("work_order holds one entry per row")
-    _launch("ress_masked_attn", dev, stream, ctypes.byref(s), ctypes.byref(m),
-            _sized(q, (B, H, n, 64), bf, dev, "q"), _sized(k, (B, H, N, 64), bf, dev, "k"),
-            _sized(v, (B, H, N, 64), bf, dev, "v"),
-            _sized(kv_idx, (B, H, nq, nk), i32, dev, "kv_idx"),
-            _sized(kv_cnt, (B, H, nq), i32, dev, "kv_cnt"), _ptr(work_order), float(scale),
-            _sized(out, (B, H, n, 64), bf, dev, "out"), _sized(lse, (B, H, n), f32, dev, "lse"),
-            _ptr(workspace), nbytes, _ptr(dev_err))
+    if work_order is not None and (work_order.numel() != B * H * nq or work_order.dtype != i32
+                                   or work_order.device != dev):
+        raise ValueError("work_order holds one int32 entry per row")
+    if dev_err is not None and (dev_err.dtype != i32 or dev_err.device != dev):
+        raise ValueError("dev_err is an int32 word on the tensors' device")
+    rows, keys = (B, H, n, 64), (B, H, N, 64)
+    _launch("ress_masked_attn", dev, stream, s, m, _sized(q, rows, bf, dev, "q"),
+            _sized(k, keys, bf, dev, "k"), _sized(v, keys, bf, dev, "v"),
+            None if kv_idx is None else _sized(kv_idx, (B, H, nq, nk), i32, dev, "kv_idx"),
+            None if kv_cnt is None else _sized(kv_cnt, (B, H, nq), i32, dev, "kv_cnt"),
+            None if work_order is None else _ptr(work_order), scale,
+            _sized(out, rows, bf, dev, "out"), _sized(lse, (B, H, n), f32, dev, "lse"),
+            _ptr(workspace), nbytes, None if dev_err is None else _ptr(dev_err))

@@ -110,7 +110,7 @@ def test_qk_refusals(lib):
     plan = R.rope_plan(64)
 
     def call(v=None, v_out=None, q=None, q_out=None, k_out=None, **kw):
-        p = R.ress_qk_params(1, 10, 2, 2, 64, 0, 1, 1e-6, None, None, None, None, ctypes.pointer(plan), None, 0,
+        p = R.ress_qk_params(1, 10, 2, 2, 64, 0, 1, 1e-6, None, None, None, None, ctypes.addressof(plan), None, 0,
                              1, 0)
         for n, x in kw.items():
             setattr(p, n, x)
