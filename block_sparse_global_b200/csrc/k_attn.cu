@@ -29,7 +29,13 @@
 // 700 clock cycles of tensor-core work.  Two of every eight column pairs therefore take
 // exp2 on the FMA and integer pipes instead (range reduction plus a fitted polynomial,
 // see exp2_pair_fma); the rest use MUFU ex2.approx.f32.
-#include "k_attn.cuh"
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
+#include <mutex>
+
+#include "ress_common.cuh"
 #include "ress_internal.h"
 
 namespace ress {
@@ -70,7 +76,35 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 256, "barriers fit their shared-memory slot");
 
+// Shared-memory matrix descriptor, 128-byte swizzle, 8-row groups 1024 bytes apart.
+RESS_DEV uint64_t smem_desc(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)64 << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
 // ---------------------------------------------------------------- softmax arithmetic
+// Two fp32 values in one 64-bit register, for the packed f32x2 FMA-pipe instructions.
+RESS_DEV uint64_t f2(float lo, float hi) {
+  return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
+}
+RESS_DEV float f2lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
+RESS_DEV float f2hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+RESS_DEV uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+RESS_DEV uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+RESS_DEV float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // 2^x for a pair, on the FMA / integer pipes instead of the MUFU unit.  Range reduction
 // to nearest: x = j + f with j = round(x) (adding 1.5 * 2^23 rounds to an integer in the
 // low mantissa bits), f in [-1/2, 1/2]; 2^f from a degree-3 polynomial fitted here for
@@ -100,6 +134,13 @@ RESS_DEV uint64_t exp2_pair_fma(uint64_t x) {
 #define RESS_POLY_PAIRS_PER8 2
 #endif
 constexpr int kPolyPairsPer8 = RESS_POLY_PAIRS_PER8;
+
+// Instruction descriptors, kind::f16: bf16 A and B, fp32 accumulator.
+//   S  = Q K^T : M = 128, N = 128, A and B K-major.
+//   O += P V   : M = 128, N = 64, A from tensor memory, B (V) MN-major.
+constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t kIdescPV =
+    (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
 
 struct AttnParams {
   const int32_t *kv_idx, *kv_cnt, *order;
@@ -437,6 +478,35 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+// [B*H, N, 64] bf16 viewed as a 3-D tensor (64, N, B*H); box (64, rows, 1); rows past N
+// read as zero.
+bool make_map(CUtensorMap *m, const void *base, int N, long long BH, int rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {64, (cuuint64_t)N, (cuuint64_t)BH};
+  cuuint64_t strides[2] = {128, (cuuint64_t)N * 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
 }
 
 }  // namespace

@@ -1,5 +1,7 @@
-// Pieces that the attention kernels share: matrix descriptors of 128 x 64 bf16 tiles,
-// packed fp32 arithmetic of the softmax, and tensor maps of [B*H, n, 64] tensors.
+// Pieces of the attention kernels with changed scores: matrix descriptors of 128 x 64 bf16
+// tiles, packed fp32 arithmetic of the softmax, and tensor maps of [B*H, n, 64] tensors.
+// k_attn.cu keeps its own copies of most of them: its recorded DRAM traffic is tied to the
+// bytes of that file.
 #pragma once
 
 #include <cuda.h>

@@ -30,6 +30,13 @@
 // warps look at the values of every tile that is not whole for all of them; those that are
 // not finite are added by hand to the rows that see their token, and replaced by 0 in shared
 // memory before the product.  Finite inputs pay 64 tests per row for this.
+//
+// What bounds it: as in k_attn.cu the softmax warps, two a scheduler, whose dependent chains do
+// not hide one another; the exponentials alone take 1024 of about 1870 clocks per tile and SM.
+// Measured on one B200, 16 heads x 10992 tokens, every block: 754 us plain (653 TFLOP/s), 902
+// with a bias by view, 908 capped at 50, 1780 capped at 10 (scores beyond the polynomials), 464
+// causal over views, 404 causal; 43968 tokens causal over views and capped 7.1 ms (574
+// TFLOP/s of visible pairs).
 #include <algorithm>
 #include <climits>
 

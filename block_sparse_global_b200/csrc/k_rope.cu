@@ -19,6 +19,10 @@
 // What bounds it: HBM.  Every element is read and written once.  The angles of a token are
 // the same for every head, so a CTA takes some tokens with all their heads, computes their
 // angles once into shared memory, and its warps then walk (heads, token) pieces.
+//
+// Measured on one B200 (in a CUDA graph): rotation of 16 heads x 137400 tokens x 64, fp16
+// (563 MB) 111 us = 5.1 TB/s; layer norm, two-axis rotation and values of 3 x 16 heads x
+// 137400 tokens, bf16 (1.69 GB) 338 us = 5.0 TB/s, of 10992 tokens (135 MB) 33 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
