@@ -597,8 +597,9 @@ ress_status ress_masked_attn(const ress_shape *shape, const ress_attn_mods *mods
   ress_attn_mods m = {};
   m.q_len = d.N;
   if (mods != nullptr) m = *mods;
-  if (m.q_len < 0 || !(m.softcap >= 0.f) || std::isinf(m.softcap)) return RESS_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || std::isinf(scale)) return RESS_ERR_INVALID_ARG;
+  if (m.q_len < 0 || !(m.softcap >= 0.f)) return RESS_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !(scale <= 1e30f) || !(m.softcap <= 1e30f)) return RESS_ERR_INVALID_ARG;
+  if (m.softcap > 0.f && !(scale / m.softcap >= 1e-20f && scale / m.softcap <= 1e20f)) return RESS_ERR_INVALID_ARG;
   if ((m.q_pos == nullptr) != (m.k_pos == nullptr) || (m.q_doc == nullptr) != (m.k_doc == nullptr) ||
       (m.q_order == nullptr) != (m.k_order == nullptr))
     return RESS_ERR_INVALID_ARG;

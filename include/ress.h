@@ -528,8 +528,8 @@ ress_status ress_qk_norm_rope(const ress_qk_params *params, const ress_rows *q,
  * alignment only, so that q_* may be the end of k_*. */
 typedef struct {
   int32_t q_len;                  /* Nq >= 0: query tokens of each batch element            */
-  float softcap;                  /* c >= 0, finite: scores become c tanh(score / c); 0: as
-                                     they are                                                */
+  float softcap;                  /* c: scores become c tanh(score / c); 0: as they are.  At
+                                     most 1e30, with scale / c between 1e-20 and 1e20        */
   const float *slopes;            /* DEVICE fp32 [H], finite: slopes[h] * |q_pos - k_pos| is
                                      taken off the (capped) scores; needs q_pos and k_pos    */
   const int32_t *q_pos, *k_pos;   /* positions, |pos| <= 2^24 (beyond, distances round)      */
@@ -564,6 +564,7 @@ size_t ress_masked_attn_workspace_bytes(const ress_shape *shape, int32_t q_len);
  *   work_order int32 [B*H*nq] permutation or NULL: an order of the library's own (rows that
  *            see most first, where that pays).  Outputs do not depend on it.  Calls of few
  *            rows do not look at it; otherwise an entry out of range is reported by dev_err.
+ *   scale    > 0, at most 1e30.
  *   mods     HOST; NULL: q_len = N and scores as they are.
  *   workspace  DEVICE scratch of at least ress_masked_attn_workspace_bytes(shape, q_len)
  *            bytes, 16-byte aligned, overwritten; calls that may overlap in time need one
