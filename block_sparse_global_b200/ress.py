@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional, Sequence
 
@@ -118,8 +119,7 @@ _SIGS = {
     "ress_rope": (_I32, [ctypes.POINTER(ress_rope_plan), _I32, _I32, _I32, _I32,
                          ctypes.POINTER(ress_rows), _VP, ctypes.c_int64, _I32,
                          ctypes.POINTER(ress_rows), _VP]),
-    "ress_qk_norm_rope": (_I32, [ctypes.POINTER(ress_qk_params)] + [ctypes.POINTER(ress_rows)] * 6
-                          + [_VP]),
+    "ress_qk_norm_rope": (_I32, [_VP] * 8),
 }
 
 
@@ -338,15 +338,15 @@ def rope_plan(head_dim: int, rot_dim: Optional[int] = None, axes: int = 1, layou
     return plan
 
 
-def _rows(t: torch.Tensor, shape, dtype, device) -> ress_rows:
-    """A [B, heads, N, D] tensor of this shape, type and device as strided rows."""
+def _rows(t: torch.Tensor, shape, dtype, device):
+    """A [B, heads, N, D] tensor of this shape, type and device as the fields of ress_rows."""
     if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"expected {dtype} {tuple(shape)} on {device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     b, h, n, e = t.stride()
     if e != 1 and shape[3] > 1:
         raise ValueError("the elements of a row must be contiguous")
-    return ress_rows(t.data_ptr() or None, b, h, n)
+    return t.data_ptr(), b, h, n
 
 
 def _positions(plan, positions, batch: int, tokens: int, device):
@@ -395,16 +395,25 @@ def ress_rope(plan, x: torch.Tensor, positions: Optional[torch.Tensor], out: tor
     shape, dtype, dev = x.shape, x.dtype, x.device
     if len(shape) != 4 or shape[3] != plan.head_dim or dtype not in DTYPES:
         raise ValueError(f"expected [B, heads, N, {plan.head_dim}] of bf16, fp16 or fp32")
-    src, dst = _rows(x, shape, dtype, dev), _rows(out, shape, dtype, dev)
+    src, dst = ress_rows(*_rows(x, shape, dtype, dev)), ress_rows(*_rows(out, shape, dtype, dev))
     b, h, n, _ = shape
     pos, pos_b = _positions(plan, positions, b, n, dev)
     _launch("ress_rope", dev, stream, plan, b, h, n, DTYPES[dtype], src, pos, pos_b,
             1 if inverse else 0, dst)
 
 
+class _QkBlock(ctypes.Structure):
+    _fields_ = [("params", ress_qk_params), ("rows", ress_rows * 6)]
+
+
+_QK_PACK = struct.Struct("=7if6Qq2i" + "Q3q" * 6)
+_QK_ROWS_AT = _QkBlock.rows.offset
+assert _QK_PACK.size == ctypes.sizeof(_QkBlock) and ctypes.sizeof(ress_rows) == 32
+
+
 def _affine(w: Optional[torch.Tensor], dim: int, device):
     if w is None:
-        return None
+        return 0
     if w.dtype != torch.float32 or w.shape != (dim,) or w.device != device or not w.is_contiguous():
         raise ValueError(f"norm weights and biases must be fp32 [{dim}] on the tensors' device")
     return w.data_ptr()
@@ -425,13 +434,19 @@ def ress_qk_norm_rope(q, k, q_out, k_out, v=None, v_out=None, norm: int = NORM_R
     if kv[0] != b or kv[2] != n or kv[3] != d:
         raise ValueError(f"q {tuple(shape)} and k {tuple(kv)} do not belong together")
     pos, pos_b = (None, 0) if plan is None else _positions(plan, positions, b, n, dev)
-    p = ress_qk_params(b, n, h, kv[1], d, DTYPES[dtype], norm, eps, _affine(q_weight, d, dev),
-                       _affine(q_bias, d, dev), _affine(k_weight, d, dev), _affine(k_bias, d, dev),
-                       None if plan is None else ctypes.addressof(plan), pos, pos_b, views, specials)
-    _launch("ress_qk_norm_rope", dev, stream, p, _rows(q, shape, dtype, dev),
-            _rows(k, kv, dtype, dev), None if v is None else _rows(v, kv, dtype, dev),
-            _rows(q_out, shape, dtype, dev), _rows(k_out, kv, dtype, dev),
-            None if v_out is None else _rows(v_out, kv, dtype, dev))
+    none = (0, 0, 0, 0)
+    block = _QkBlock()  # the structs of the call, filled at once
+    _QK_PACK.pack_into(
+        block, 0, b, n, h, kv[1], d, DTYPES[dtype], norm, eps, _affine(q_weight, d, dev),
+        _affine(q_bias, d, dev), _affine(k_weight, d, dev), _affine(k_bias, d, dev),
+        0 if plan is None else ctypes.addressof(plan), pos or 0, pos_b, views, specials,
+        *_rows(q, shape, dtype, dev), *_rows(k, kv, dtype, dev),
+        *(none if v is None else _rows(v, kv, dtype, dev)), *_rows(q_out, shape, dtype, dev),
+        *_rows(k_out, kv, dtype, dev), *(none if v is None else _rows(v_out, kv, dtype, dev)))
+    at = ctypes.addressof(block)
+    q_at = at + _QK_ROWS_AT
+    _launch("ress_qk_norm_rope", dev, stream, at, q_at, q_at + 32, None if v is None else q_at + 64,
+            q_at + 96, q_at + 128, None if v is None else q_at + 160)
 
 
 # ------------------------------------------------------- attention with changed scores
