@@ -952,6 +952,8 @@ __global__ void __launch_bounds__(256) summary_kernel(const int32_t *__restrict_
 // a launch order of the longest rows first.
 __global__ void __launch_bounds__(256) plan_kernel(const __grid_constant__ Params p, long long rows,
                                                    int32_t *__restrict__ count) {
+  launch_dependents();
+  wait_prerequisites();
   const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (item >= rows) return;
@@ -981,6 +983,32 @@ __global__ void __launch_bounds__(256) plan_kernel(const __grid_constant__ Param
   if (lane == 0) count[item] = n;
 }
 
+// Up to kRankRows rows in descending order of their counts, equal ones by index: every row
+// counts those before it, four lanes a row, 64 rows a CTA.  A new view over 32 views (176 rows
+// of 687 blocks) takes 183 us with it and 191 with the sort by counters; 1376 rows of 86
+// blocks 209 and 203, so it ends at 1024.
+constexpr int kRankRows = 1024, kRankRowsOfCta = 64;
+__global__ void __launch_bounds__(256) rank_kernel(const int32_t *__restrict__ count, int n,
+                                                   int32_t *__restrict__ order) {
+  __shared__ __align__(16) int all[kRankRows + 16];
+  launch_dependents();
+  wait_prerequisites();
+  const int padded = (n + 15) & ~15;
+  for (int i = threadIdx.x; i < padded; i += 256) all[i] = i < n ? count[i] : INT_MIN;
+  __syncthreads();
+  const int i = blockIdx.x * kRankRowsOfCta + (threadIdx.x >> 2), part = threadIdx.x & 3;
+  const int own = i < n ? all[i] : 0;
+  int rank = 0;
+  for (int j = 4 * part; j < padded; j += 16) {
+    const int4 c = *reinterpret_cast<const int4 *>(&all[j]);
+    rank += (c.x > own || (c.x == own && j < i)) + (c.y > own || (c.y == own && j + 1 < i)) +
+            (c.z > own || (c.z == own && j + 2 < i)) + (c.w > own || (c.w == own && j + 3 < i));
+  }
+  rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+  rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+  if (i < n && part == 0) order[rank] = i;
+}
+
 // Rows of a problem without keys: zero, and lse = -inf.
 __global__ void __launch_bounds__(256) no_keys_kernel(long long rows, uint4 *__restrict__ out,
                                                       float *__restrict__ lse) {
@@ -994,8 +1022,8 @@ __global__ void __launch_bounds__(256) no_keys_kernel(long long rows, uint4 *__r
 // tiles of the longest possible row; long rows (16 tiles a part) are split on into up to four
 // times as many, since kept lists and masks make them uneven.  A part's sums cost 32 KB each
 // way and the join a dependent launch: 4 heads of 1024 tokens, causal with a prefix, 16.6 us
-// at 2 tiles a part, 17.8 at 4, 19.0 unsplit; a new view over 32 views 315 us unsplit, 204 at
-// four parts.
+// at 2 tiles a part, 17.8 at 4, 19.0 unsplit; a new view over 32 views 315 us unsplit, 215 at
+// four parts (before the order below).
 constexpr int kSlots = 2 * 148, kTilesPerSplit = 2, kTilesOfUneven = 16;
 int splits_of(const Dims &d, int nq) {
   const long long items = d.BH() * nq;
@@ -1007,8 +1035,8 @@ int splits_of(const Dims &d, int nq) {
 }
 
 // Rows of masked calls and of kept lists are put in order, longest first, where they come in
-// more than one wave and are long enough for the tail to matter (one or two small kernels,
-// about 5 us each).
+// more than one wave and are long enough for the tail to matter (one or two small kernels
+// of 3-6 us).
 bool plans_order(const Dims &d, int nq) {
   const long long items = d.BH() * nq;
   return items * splits_of(d, nq) > kSlots && items * ((d.N + 127) / 128) >= 64 * kSlots;
@@ -1130,13 +1158,19 @@ cudaError_t launch_masked_attn(const Dims &d, const MaskedAttnLaunch &a, cudaStr
   const bool masked = m.q_doc || m.q_order;
   if (sorted && !p.order && (masked || p.kv_cnt)) {
     if (masked) {
-      plan_kernel<<<(unsigned)((items + 7) / 8), 256, 0, st>>>(p, items, count);
-      cudaError_t e = cudaGetLastError();
+      cudaError_t e = launch_after(plan_kernel, dim3((unsigned)((items + 7) / 8)), 256, 0, st, true, p, items, count);
       if (e != cudaSuccess) return e;
     }
-    Dims rows = d;
-    rows.nb = rows.nq = nq;
-    cudaError_t e = launch_schedule(rows, masked ? count : p.kv_cnt, sorted, st);
+    const int32_t *by = masked ? count : p.kv_cnt;
+    cudaError_t e;
+    if (items <= kRankRows) {
+      const unsigned ctas = (unsigned)((items + kRankRowsOfCta - 1) / kRankRowsOfCta);
+      e = launch_after(rank_kernel, dim3(ctas), 256, 0, st, masked || m.slopes, by, (int)items, sorted);
+    } else {
+      Dims rows = d;
+      rows.nb = rows.nq = nq;
+      e = launch_schedule(rows, by, sorted, st);
+    }
     if (e != cudaSuccess) return e;
     p.order = sorted;
   }

@@ -216,6 +216,7 @@ def test_against_64_bits(Bn, H, N, Nq, kb, keep, cap, docs, pad, order, bias, sh
 @pytest.mark.gpu
 @pytest.mark.parametrize("Bn,H,N,Nq,kb,keep,cap,docs,pad,order,bias", [
     (1, 16, 8000, 8000, 128, 0.5, 0.0, 3, 150, "none", 0.0), (2, 6, 7777, 7777, 64, 0.5, 30.0, 2, 33, "token", 0.01),
+    (1, 20, 7000, 7000, 128, 0.3, 0.0, 0, 0, "view", 0.0),
     (1, 16, 9000, 1500, 128, 0.5, 0.0, 2, 100, "token", 0.0), (1, 16, 9001, 1374, 64, 0.25, 0.0, 0, 0, "view", 0.02)])
 def test_many_rows_and_long_rows(Bn, H, N, Nq, kb, keep, cap, docs, pad, order, bias):
     """Rows enough to be put in order by what they see, and rows long enough for several parts."""
