@@ -124,7 +124,9 @@ RESS_DEV void cap_any(uint32_t (&sv)[128], float in) {
 
 // Programmatic dependent launch: a kernel's CTAs may start while the kernel before it still
 // runs, once all of that one's CTAs have called launch_dependents (or ended), and wait for its
-// results where they need them.  Without the launch attribute both do nothing.
+// results where they need them.  Without the launch attribute both do nothing.  Such results are
+// never read as constants (__ldg, const __restrict__): they are still being written when the
+// reader starts, and the read-only path may serve a load from before the wait.
 RESS_DEV void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 RESS_DEV void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -500,8 +502,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             // (summaries are 16 bytes a block: eight of them to a line of L1)
             const volatile uint16_t *own = list + vb->skip + (KB == 128 ? j : 2 * j);
             const int4 *sum = p.blocks + (long long)(p.B + vb->b) * p.nk;
-            const int4 p0 = __ldg(sum + own[0]);  // smallest, largest, first, step
-            const int4 p1 = KB == 64 && 2 * j + 1 < vb->entries ? __ldg(sum + own[1]) : p0;
+            const int4 p0 = sum[own[0]];  // smallest, largest, first, step
+            const int4 p1 = KB == 64 && 2 * j + 1 < vb->entries ? sum[own[1]] : p0;
             const int lo = min(p0.x, p1.x), hi = max(p0.y, p1.y);
             side = hi <= q_lo ? 1 : (lo >= q_hi ? -1 : 0);
             even = side != 0 && p0.w != kUneven && p1.w != kUneven;
@@ -851,10 +853,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 // One warp per query row: out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.  A split with
 // l = 0 saw no key (its O is not written); one with l < 0 met an error and leaves the row
 // as it was.  A lane weighs a split, so that the O's loads depend on nothing but the weights.
-__global__ void __launch_bounds__(256) join_kernel(const float *__restrict__ part_o,
-                                                   const float2 *__restrict__ part_ml, int splits, int nq,
-                                                   int Nq, long long rows, __nv_bfloat16 *__restrict__ out,
-                                                   float *__restrict__ lse) {
+__global__ void __launch_bounds__(256) join_kernel(const float *part_o, const float2 *part_ml, int splits, int nq,
+                                                   int Nq, long long rows, __nv_bfloat16 *out, float *lse) {
   wait_prerequisites();
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -951,7 +951,7 @@ __global__ void __launch_bounds__(256) summary_kernel(const int32_t *__restrict_
 // Rows of a masked call, one warp each: how many of the row's kept blocks some query sees, for
 // a launch order of the longest rows first.
 __global__ void __launch_bounds__(256) plan_kernel(const __grid_constant__ Params p, long long rows,
-                                                   int32_t *__restrict__ count) {
+                                                   int32_t *count) {
   launch_dependents();
   wait_prerequisites();
   const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -988,8 +988,7 @@ __global__ void __launch_bounds__(256) plan_kernel(const __grid_constant__ Param
 // of 687 blocks) takes 183 us with it and 191 with the sort by counters; 1376 rows of 86
 // blocks 209 and 203, so it ends at 1024.
 constexpr int kRankRows = 1024, kRankRowsOfCta = 64;
-__global__ void __launch_bounds__(256) rank_kernel(const int32_t *__restrict__ count, int n,
-                                                   int32_t *__restrict__ order) {
+__global__ void __launch_bounds__(256) rank_kernel(const int32_t *count, int n, int32_t *order) {
   __shared__ __align__(16) int all[kRankRows + 16];
   launch_dependents();
   wait_prerequisites();
