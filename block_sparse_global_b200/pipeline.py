@@ -7,6 +7,8 @@
 Every step runs in the library's kernels; this class only owns the buffers and orders
 the calls on one stream: pool -> block map + selection (one kernel; for the drift method
 the block map, drift score and restoration rounds in one kernel) -> schedule -> attention.
+The buffers are made on the stream that is current at construction, those that a call makes
+for itself on the call's; a layer has to outlive the work it enqueued on other streams.
 """
 from __future__ import annotations
 
@@ -53,6 +55,23 @@ class SparseGlobalAttention:
         self._qkv = None      # prepare()'s outputs
         self._masked_ws = {}  # attend_masked()'s workspaces
 
+    def _empty(self, shape, dtype, stream):
+        """A tensor for a call on `stream` (None: the current one), made on that stream: the
+        allocator may hand out memory that work enqueued earlier still uses, and it orders
+        only the stream that the tensor is made on behind that work.  The caller's current
+        stream is noted as a user of it."""
+        device = self.out.device
+        if stream is None:
+            return torch.empty(shape, device=device, dtype=dtype)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        current = torch.cuda.current_stream(device)
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, device=device, dtype=dtype)
+        if stream.cuda_stream != current.cuda_stream:
+            t.record_stream(current)
+        return t
+
     def load_output_projection(self, w_o: torch.Tensor, stream=None):
         """M_h = W_O^h^T W_O^h for every head (ReSS Eq. 8), computed once per layer."""
         R.ress_head_gram(self.shape, w_o.contiguous().float(), self.gram, stream)
@@ -64,16 +83,16 @@ class SparseGlobalAttention:
         per-head norm and the rotary positions of q and k, and the move of every view's
         special tokens to the tail, in one pass.  The three tensors belong to the layer and
         are overwritten by the next call."""
-        if self._qkv is None:
-            self._qkv = [torch.empty(self.B, self.H, self.N, 64, device=self.device,
-                                     dtype=torch.bfloat16) for _ in range(3)]
         if packed.shape != (self.B, self.N, 3, self.H, 64):
             raise ValueError(f"expected a packed projection [B,N,3,H,64], got {tuple(packed.shape)}")
         q, k, v = (packed[:, :, i].transpose(1, 2) for i in range(3))
-        q_out, k_out, v_out = self._qkv
+        made = self._qkv or [self._empty((self.B, self.H, self.N, 64), torch.bfloat16, stream)
+                             for _ in range(3)]
+        q_out, k_out, v_out = made
         R.ress_qk_norm_rope(q, k, q_out, k_out, v, v_out, norm=norm, eps=eps, q_weight=q_weight,
                             q_bias=q_bias, k_weight=k_weight, k_bias=k_bias, plan=plan,
                             positions=positions, views=views, specials=specials, stream=stream)
+        self._qkv = made  # (not before: a refused call leaves them to no stream)
         return q_out, k_out, v_out
 
     # ------------------------------------------------------------------ the path
@@ -142,7 +161,8 @@ class SparseGlobalAttention:
         for ress_masked_attn) of q [B,H,q_len,64] over this layer's k, v.  kept: over the
         selected blocks, for all of the sequence's tokens (q_len = N); otherwise over every
         block, for any q_len (new tokens over a cache).  Without `out`, the result goes to
-        the layer's out and lse if q_len = N, else to a new tensor.  The layer keeps one
+        the layer's out and lse if q_len = N, else to a new tensor (made on `stream`; the
+        current stream has to wait for the call before it reads it).  The layer keeps one
         workspace per number of query blocks, for eager calls and captured graphs alike:
         such calls of one layer must not overlap in time."""
         n = q.shape[2]
@@ -152,16 +172,15 @@ class SparseGlobalAttention:
             if n == self.N:
                 out, lse = self.out, self.lse if lse is None else lse
             else:
-                out = torch.empty(self.B, self.H, n, 64, device=self.device, dtype=torch.bfloat16)
-        # kept for good: a captured graph holds its address
+                out = self._empty((self.B, self.H, n, 64), torch.bfloat16, stream)
         ws = self._masked_ws.get((n + 127) // 128)
         if ws is None:
             need = R.ress_masked_attn_workspace_bytes(self.shape, (n + 127) // 128 * 128)
-            ws = torch.empty(max(need, 16), device=self.device, dtype=torch.uint8)
-            self._masked_ws[(n + 127) // 128] = ws
+            ws = self._empty((max(need, 16),), torch.uint8, stream)
         R.ress_masked_attn(self.shape, q, k, v, self.kv_idx if kept else None,
                            self.kv_cnt if kept else None, None, self.scale, out, lse, workspace=ws,
                            dev_err=self.dev_err[:1], stream=stream, **mods)
+        self._masked_ws[(n + 127) // 128] = ws  # kept for good: a captured graph holds its address
         return out
 
     def forward(self, q, k, v, method: int, budgets: Sequence[int], keep_k=None, dense_q=None,
