@@ -12,6 +12,7 @@ for itself on the call's; a layer has to outlive the work it enqueued on other s
 """
 from __future__ import annotations
 
+import contextlib
 import math
 from typing import Optional, Sequence
 
@@ -61,20 +62,25 @@ class SparseGlobalAttention:
         only the stream that the tensor is made on behind that work.  The caller's current
         stream is noted as a user of it."""
         device = self.out.device
-        if stream is None:
-            return torch.empty(shape, device=device, dtype=dtype)
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        current = torch.cuda.current_stream(device)
-        with torch.cuda.stream(stream):
+        with self._on(stream):
             t = torch.empty(shape, device=device, dtype=dtype)
-        if stream.cuda_stream != current.cuda_stream:
-            t.record_stream(current)
+        if stream is not None:
+            t.record_stream(torch.cuda.current_stream(device))  # (no-op on the stream it was made on)
         return t
+
+    def _on(self, stream):
+        """The stream of a call (torch's or a handle; None: the current one) as torch's current."""
+        if stream is None:
+            return contextlib.nullcontext()
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.out.device)
+        return torch.cuda.stream(stream)
 
     def load_output_projection(self, w_o: torch.Tensor, stream=None):
         """M_h = W_O^h^T W_O^h for every head (ReSS Eq. 8), computed once per layer."""
-        R.ress_head_gram(self.shape, w_o.contiguous().float(), self.gram, stream)
+        with self._on(stream):  # a converted copy belongs to the stream that reads it
+            w_o = w_o.contiguous().float()
+        R.ress_head_gram(self.shape, w_o, self.gram, stream)
 
     def prepare(self, packed, plan=None, positions=None, norm: int = R.NORM_NONE, eps: float = 1e-6,
                 q_weight=None, q_bias=None, k_weight=None, k_bias=None, views: int = 1,

@@ -82,6 +82,16 @@ def test_prepared_tensors_are_made_on_the_calls_stream(fake):
         assert fake.made[t.data_ptr()] == 9 and 0 in fake.used[t.data_ptr()]
 
 
+def test_projection_is_converted_on_the_calls_stream(fake, monkeypatch):
+    layer = P.SparseGlobalAttention(1, 2, 300, device="cpu")
+    real, where = torch.Tensor.float, []
+    monkeypatch.setattr(torch.Tensor, "float", lambda t: where.append(fake.now.cuda_stream) or real(t))
+    monkeypatch.setattr(R, "ress_head_gram", lambda *a: None)
+    layer.load_output_projection(torch.zeros(128, 128, dtype=BF16), stream=FakeStream(5))
+    layer.load_output_projection(torch.zeros(128, 128, dtype=BF16))
+    assert where == [5, 0]
+
+
 def test_a_refused_call_leaves_no_buffer_behind(fake, monkeypatch):
     """A buffer of a call that never ran would belong to a stream that nothing is ordered by."""
     layer = P.SparseGlobalAttention(1, 2, 3000, device="cpu")
