@@ -432,16 +432,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t trow = vb->tmem_base + ((uint32_t)(warp * 32) << 16);
         int *m_doc = reinterpret_cast<int *>(smem + kOffMeta), *m_order = m_doc + 128;
         float *m_pos = reinterpret_cast<float *>(smem + kOffPos) + warp * 128;
-        // positions relative to the row block's first query: exact small numbers
-        int ref = 0, q_lo = 0, q_hi = 0;  // and the range of the warp's queries
-        float row_pos = 0.f, slope = 0.f;
+        int q_pos = 0, q_lo = 0, q_hi = 0;  // this query's position, and the range of the warp's
+        float slope = 0.f;
         if constexpr (BIAS) {
-          const int32_t *qp = p.q_pos + (long long)vb->b * p.Nq;
-          ref = qp[vb->qi * 128];
-          const int mine_pos = qp[min(vb->qi * 128 + tid, p.Nq - 1)];
-          q_lo = __reduce_min_sync(0xffffffffu, mine_pos);
-          q_hi = __reduce_max_sync(0xffffffffu, mine_pos);
-          row_pos = (float)((long long)mine_pos - ref);
+          q_pos = p.q_pos[(long long)vb->b * p.Nq + min(vb->qi * 128 + tid, p.Nq - 1)];
+          q_lo = __reduce_min_sync(0xffffffffu, q_pos);
+          q_hi = __reduce_max_sync(0xffffffffu, q_pos);
           slope = -p.slopes[vb->bh % p.H] * kLog2e;
         }
         // key of column c of tile j, or -1
@@ -494,10 +490,15 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           // The bias of column c of half i, where the keys lie on one side of the warp's
           // queries: shift[i] + step[i] (c mod 64) if positions run evenly in each half (the
-          // usual case: tokens, or all of one view), else shift[i] + m_pos[c].
+          // usual case: tokens, or all of one view), else shift[i] + m_pos[c].  m_pos is
+          // measured from the warp's query that the keys are nearest to: both terms then have
+          // the distance's sign, and neither is larger, so that nothing cancels wherever the
+          // block's other queries are.  On both sides, from the middle of all of the
+          // positions: differences from it are exact up to the documented 2^24.
           float shift[2] = {0.f, 0.f}, step[2] = {0.f, 0.f};
           int side = 0;  // +1: every key at or before every query, -1: at or after, 0: mixed
           bool even = true;
+          float row_pos = 0.f;
           if constexpr (BIAS) {
             // (summaries are 16 bytes a block: eight of them to a line of L1)
             const volatile uint16_t *own = list + vb->skip + (KB == 128 ? j : 2 * j);
@@ -511,9 +512,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (even) {
               step[0] = f * (float)p0.w;
               step[1] = f * (float)p1.w;
-              shift[0] = f * ((float)((long long)p0.z - ref) - row_pos);
-              shift[1] = KB == 64 ? f * ((float)((long long)p1.z - ref) - row_pos) : fmaf(64.0f, step[0], shift[0]);
+              shift[0] = f * (float)((long long)p0.z - q_pos);
+              shift[1] = KB == 64 ? f * (float)((long long)p1.z - q_pos) : fmaf(64.0f, step[0], shift[0]);
             } else {
+              const int ref = side > 0 ? q_lo : (side < 0 ? q_hi : (int)(((long long)min(q_lo, lo) + max(q_hi, hi)) >> 1));
+              row_pos = (float)((long long)q_pos - ref);
               shift[0] = shift[1] = side == 0 ? 0.f : -f * row_pos;
               __syncwarp();  // the last tile's have been read
               for (int c = lane; c < 128; c += 32) {
