@@ -489,15 +489,16 @@ __global__ void __launch_bounds__(kThreads, 2)
             meet();
           }
           // The bias of column c of half i, where the keys lie on one side of the warp's
-          // queries: shift[i] + step[i] (c mod 64) if positions run evenly in each half (the
-          // usual case: tokens, or all of one view), else shift[i] + m_pos[c].  m_pos is
-          // measured from the warp's query that the keys are nearest to: both terms then have
-          // the distance's sign, and neither is larger, so that nothing cancels wherever the
-          // block's other queries are.  On both sides, from the middle of all of the
-          // positions: differences from it are exact up to the documented 2^24.
+          // queries: shift[i] + step[i] (c mod 64 - end) if positions run evenly in each half
+          // (the usual case: tokens, or all of one view), else shift[i] + m_pos[c].  end is
+          // the column of a half's key nearest to the queries, 0 or 63; m_pos is measured from
+          // the warp's query nearest to the keys: both terms have the distance's sign,
+          // and neither is larger, so that nothing cancels however far the tile reaches and
+          // wherever the block's other queries are.  On both sides, from the middle of all
+          // of the positions: differences from it are exact up to the documented 2^24.
           float shift[2] = {0.f, 0.f}, step[2] = {0.f, 0.f};
           int side = 0;  // +1: every key at or before every query, -1: at or after, 0: mixed
-          bool even = true;
+          bool even = true, last = false;  // last: end = 63
           float row_pos = 0.f;
           if constexpr (BIAS) {
             // (summaries are 16 bytes a block: eight of them to a line of L1)
@@ -507,13 +508,15 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int4 p1 = KB == 64 && 2 * j + 1 < vb->entries ? sum[own[1]] : p0;
             const int lo = min(p0.x, p1.x), hi = max(p0.y, p1.y);
             side = hi <= q_lo ? 1 : (lo >= q_hi ? -1 : 0);
-            even = side != 0 && p0.w != kUneven && p1.w != kUneven;
+            even = side != 0 && p0.w != kUneven && p1.w != kUneven && (p0.w >= 0) == (p1.w >= 0);
+            last = side > 0 ? max(p0.w, p1.w) > 0 : min(p0.w, p1.w) < 0;
             const float f = side == 0 ? 1.0f : (side > 0 ? -slope : slope);
             if (even) {
               step[0] = f * (float)p0.w;
               step[1] = f * (float)p1.w;
-              shift[0] = f * (float)((long long)p0.z - q_pos);
-              shift[1] = KB == 64 ? f * (float)((long long)p1.z - q_pos) : fmaf(64.0f, step[0], shift[0]);
+              const int end = last ? 63 : 0;
+              shift[0] = f * (float)((long long)p0.z - q_pos + (long long)end * p0.w);
+              shift[1] = f * (float)((long long)p1.z - q_pos + (long long)((KB == 64 ? 0 : 64) + end) * p1.w);
             } else {
               const int ref = side > 0 ? q_lo : (side < 0 ? q_hi : (int)(((long long)min(q_lo, lo) + max(q_hi, hi)) >> 1));
               row_pos = (float)((long long)q_pos - ref);
@@ -612,21 +615,29 @@ __global__ void __launch_bounds__(kThreads, 2)
               const uint64_t sc2 = f2(sc, sc);
               if (!even || step[0] != 0.f || step[1] != 0.f) {
                 if (even) {
+                  // from the near end outwards, so that the running sum's roundings are of its
+                  // own size (a product with the column's number each: 1050 against 944 us)
+                  const auto ramp = [&](bool back) {  // (known when this is unrolled)
 #pragma unroll
-                  for (int i = 0; i < 2; ++i) {
-                    const uint64_t st = f2(8.0f * step[i], 8.0f * step[i]);
-                    uint64_t run[4];
+                    for (int i = 0; i < 2; ++i) {
+                      const float t = back ? -step[i] : step[i];
+                      const uint64_t st = f2(8.0f * t, 8.0f * t);
+                      uint64_t run[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) run[q] = f2(2 * q * step[i], (2 * q + 1) * step[i]);
+                      for (int q = 0; q < 4; ++q)
+                        run[q] = back ? f2((2 * q + 1) * t, 2 * q * t) : f2(2 * q * t, (2 * q + 1) * t);
 #pragma unroll
-                    for (int c = 64 * i; c < 64 * i + 64; c += 2) {
-                      const int q = (c >> 1) & 3;
-                      const uint64_t z = ffma2(f2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sc2, run[q]);
-                      run[q] = fadd2(run[q], st);
-                      sv[c] = (uint32_t)z;
-                      sv[c + 1] = (uint32_t)(z >> 32);
+                      for (int c = 0; c < 64; c += 2) {
+                        uint32_t *s = &sv[64 * i + (back ? 62 - c : c)];
+                        const int q = (c >> 1) & 3;
+                        const uint64_t z = ffma2(f2(__uint_as_float(s[0]), __uint_as_float(s[1])), sc2, run[q]);
+                        run[q] = fadd2(run[q], st);
+                        s[0] = (uint32_t)z;
+                        s[1] = (uint32_t)(z >> 32);
+                      }
                     }
-                  }
+                  };
+                  last ? ramp(true) : ramp(false);
                 } else if (side != 0) {
 #pragma unroll
                   for (int c = 0; c < 128; c += 4) {
@@ -907,7 +918,7 @@ __global__ void __launch_bounds__(256) join_kernel(const float *part_o, const fl
 // ------------------------------------------------------------------- block summaries
 // One warp per key block, over its tokens: {min doc, max doc, min order, max order}, and
 // {min, max, first position, step} with the step kUneven unless every position is first +
-// step * place.
+// step * place (a block short of tokens is uneven: it has no last column to measure from).
 __global__ void __launch_bounds__(256) summary_kernel(const int32_t *__restrict__ doc,
                                                       const int32_t *__restrict__ order,
                                                       const int32_t *__restrict__ pos, int N, int nk, int kb,
@@ -937,7 +948,7 @@ __global__ void __launch_bounds__(256) summary_kernel(const int32_t *__restrict_
     pos += b * N + u0;
     int lo = INT_MAX, hi = INT_MIN;
     const long long first = pos[0], step = n > 1 ? pos[1] - first : 0;
-    bool even = step > -(1 << 20) && step < (1 << 20);
+    bool even = n == kb && step > -(1 << 20) && step < (1 << 20);
     for (int u = lane; u < n; u += 32) {
       const int x = pos[u];
       lo = min(lo, x);

@@ -7,8 +7,9 @@ D the bias of the row's keys that carry weight (2^-40 of the largest, the others
 R the row's largest |score|, in units of 2^-24:
   bias    slope log2 e 2 D; a distance is a sum of two terms of one sign, each converted and
           multiplied (2 D); the score added to one (R + D), the other less the maximum
-          (D + |max|), and their sum (R + D + |max|), with |max| <= R + D
-          -> 9 D + 4 R
+          (D + |max|), and their sum (R + D + |max|), with |max| <= R + D; the key's term may be
+          a running sum of up to 15 additions of one sign, the k-th rounding k/15 of it (8 D)
+          -> 17 D + 4 R
   cap     tanh within 2^-21 of its value, products and scales 4 roundings -> 12 R
 """
 import math
@@ -64,7 +65,7 @@ def _check_rows(q, k, v, out, lse, scale=0.125, softcap=0.0, slopes=None, q_pos=
             near = s >= s.amax(-1, keepdim=True) - 40 * math.log(2)
             far[b, h] = torch.where(near & seen, d.abs(), torch.zeros_like(d)).amax(-1)
     top = reach if not softcap else reach.clamp_max(softcap)
-    e = 64 * 2.0 ** -23 * reach + (9 * far + (16 if softcap else 4) * top) * 2.0 ** -24
+    e = 64 * 2.0 ** -23 * reach + (17 * far + (16 if softcap else 4) * top) * 2.0 ** -24
     none = want_lse == -math.inf
     assert bool((lse[none] == -math.inf).all()) and bool((out[none] == 0).all())
     # exponentials 2^-21, sums a tree a tile, the logarithm's and its own rounding
@@ -100,6 +101,24 @@ def test_queries_of_a_block_far_from_one_another(cap, kb):
     N, Nq = len(k_pos), len(q_pos)
     q, k, v = _inputs(3, N, Nq, seed=3)
     mods = dict(softcap=cap, slopes=torch.tensor([0.5, 1.0, 0.01], device="cuda"),
+                q_pos=q_pos.to(torch.int32).view(1, Nq).cuda(), k_pos=k_pos.to(torch.int32).view(1, N).cuda())
+    out, lse = _run(q, k, v, kb, **mods)
+    _check_rows(q, k, v, out, lse, **mods)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kb", [64, 128])
+@pytest.mark.parametrize("side", [1, -1])
+@pytest.mark.parametrize("step", [1, 7, -1000, 40000, -40000])
+def test_evenly_spaced_positions_of_any_step(step, side, kb):
+    """Keys whose even steps are large, as time stamps are, and queries just behind or ahead of
+    them: the key next to a query is not rounded at the magnitude of its block's first one.
+    Two whole runs of the same positions and a short one."""
+    N, Nq, H = 300, 2000, 3
+    q, k, v = _inputs(H, N, Nq, seed=9)
+    k_pos = step * (torch.arange(N) % 128)
+    q_pos = (k_pos.max() if side > 0 else k_pos.min()) + side * (1 + torch.arange(Nq) % 3)
+    mods = dict(slopes=torch.tensor([0.5, 1.0, 0.01], device="cuda"),
                 q_pos=q_pos.to(torch.int32).view(1, Nq).cuda(), k_pos=k_pos.to(torch.int32).view(1, N).cuda())
     out, lse = _run(q, k, v, kb, **mods)
     _check_rows(q, k, v, out, lse, **mods)
