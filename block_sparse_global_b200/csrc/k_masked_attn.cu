@@ -111,14 +111,25 @@ RESS_DEV void cap_small(uint32_t (&sv)[128], float in) {
     sv[c + 1] = __float_as_uint(f2hi(u));
   }
 }
-// Any score: 1 - 2 / (1 + e^2y), off by an fp32 unit absolutely, which is all that the
-// exponent takes from it.
+// Any score, as tanh_any: 1 - 2 / (1 + e^2y) from |y| = 1/2 on, the polynomial below, so that
+// small scores beside large ones keep a relative error (2^-21 of each score's own).
 RESS_DEV void cap_any(uint32_t (&sv)[128], float in) {
-  const float in2 = 2.0f * kLog2e * in;
+  const float in2 = 2.0f * kLog2e * in, half = 0.5f / in;
+  const uint64_t ins = f2(in, in);
 #pragma unroll
-  for (int c = 0; c < 128; ++c) {
-    const float r = rcp_approx(1.0f + ex2_approx(__uint_as_float(sv[c]) * in2));
-    sv[c] = __float_as_uint(fmaf(-2.0f, r, 1.0f));
+  for (int c = 0; c < 128; c += 2) {
+    const float s[2] = {__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])};
+    const uint64_t y = fmul2(f2(s[0], s[1]), ins);
+    const uint64_t t = fmul2(y, y);
+    uint64_t a = f2(tanh_fit<4>(4), tanh_fit<4>(4));
+#pragma unroll
+    for (int k = 3; k >= 0; --k) a = ffma2(a, t, f2(tanh_fit<4>(k), tanh_fit<4>(k)));
+    const uint64_t u = fmul2(a, y);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float r = rcp_approx(1.0f + ex2_approx(s[i] * in2));
+      sv[c + i] = __float_as_uint(fabsf(s[i]) < half ? (i ? f2hi(u) : f2lo(u)) : fmaf(-2.0f, r, 1.0f));
+    }
   }
 }
 

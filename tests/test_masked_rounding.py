@@ -122,3 +122,22 @@ def test_evenly_spaced_positions_of_any_step(step, side, kb):
                 q_pos=q_pos.to(torch.int32).view(1, Nq).cuda(), k_pos=k_pos.to(torch.int32).view(1, N).cuda())
     out, lse = _run(q, k, v, kb, **mods)
     _check_rows(q, k, v, out, lse, **mods)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kb", [64, 128])
+@pytest.mark.parametrize("bias", [0.0, 0.1])
+@pytest.mark.parametrize("cap", [0.3, 10.0, 1e4, 1e5])
+def test_the_caps_error_is_each_scores_own(cap, bias, kb):
+    """Small scores beside ones far above the cap, in one tile: each within its own rounding of
+    the cap, which is the identity to the small ones."""
+    N, H = 500, 2
+    q, k, v = _inputs(H, N, N, seed=22)
+    q[:, :, 5::32] *= 1000 * max(1.0, cap)   # a row of every warp
+    k[:, :, 7::128] *= 30                    # and a key of every tile
+    mods = dict(softcap=cap)
+    if bias:
+        t = torch.arange(N, dtype=torch.int32, device="cuda").view(1, N)
+        mods.update(slopes=torch.full((H,), bias, device="cuda"), q_pos=t, k_pos=t)
+    out, lse = _run(q, k, v, kb, **mods)
+    _check_rows(q, k, v, out, lse, **mods)
