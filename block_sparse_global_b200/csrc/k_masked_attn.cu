@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             rescale = m_new > m_run + kRescaleLog2;
             m_use = rescale ? m_new : m_run;
           };
-          float big = 0.f;  // largest |score|, for the cap
+          float big = 0.f;  // largest |score|, for the cap of a whole tile
           bool fused = false;
           if constexpr (CAP) {
             float mc[2] = {0.f, 0.f};
@@ -589,8 +589,10 @@ __global__ void __launch_bounds__(kThreads, 2)
               for (int q = 0; q < 2; ++q)
                 mc[q] = fmax3(mc[q], fabsf(__uint_as_float(sv[c + 2 * q])), fabsf(__uint_as_float(sv[c + 2 * q + 1])));
             }
-            big = fmaxf(mc[0], mc[1]);
-            fused = !BIAS && code == kWhole && __all_sync(0xffffffffu, big <= p.cap_a);
+            // (a mixed tile's may be a hidden key's, which must not choose the visible ones'
+            // arithmetic: such a tile takes the form for any score)
+            big = code == kWhole ? fmaxf(mc[0], mc[1]) : INFINITY;
+            fused = !BIAS && __all_sync(0xffffffffu, big <= p.cap_a);
           }
           if (code == kNone) {
 #pragma unroll

@@ -141,3 +141,29 @@ def test_the_caps_error_is_each_scores_own(cap, bias, kb):
         mods.update(slopes=torch.full((H,), bias, device="cuda"), q_pos=t, k_pos=t)
     out, lse = _run(q, k, v, kb, **mods)
     _check_rows(q, k, v, out, lse, **mods)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kb", [64, 128])
+@pytest.mark.parametrize("cap", [2.0, 30.0, 1e4])
+@pytest.mark.parametrize("bias", [0.0, 0.1])
+@pytest.mark.parametrize("hidden", [float("inf"), float("nan"), 1e4])
+def test_capped_rows_do_not_change_with_keys_that_they_do_not_see(hidden, bias, cap, kb):
+    """A later key, whatever it holds, leaves every bit of the rows before it, although rows of
+    the same warp see it; so does a key that no query sees."""
+    N, H = 400, 4                            # (the form for few rows takes less)
+    q, k, v = _inputs(H, N, N, seed=21)
+    t = torch.arange(N, dtype=torch.int32, device="cuda").view(1, N)
+    doc = (t >= 390).to(torch.int32) * -1
+    mods = dict(softcap=cap, q_order=t, k_order=t, q_doc=doc, k_doc=doc)
+    if bias:
+        mods.update(slopes=torch.full((H,), bias, device="cuda"), q_pos=t, k_pos=t)
+    clean, lse = _run(q, k, v, kb, **mods)
+    _check_rows(q, k, v, clean, lse, **mods)
+    k2, v2 = k.clone(), v.clone()
+    k2[:, :, 300, 0] = hidden                # rows 288 to 299 share a warp with those that see it
+    k2[:, :, 395, 0] = hidden                # padding
+    v2[:, :, 300, 3] = hidden
+    out, lse2 = _run(q, k2, v2, kb, **mods)
+    assert torch.equal(out[:, :, :300], clean[:, :, :300]) and torch.equal(lse2[:, :, :300], lse[:, :, :300])
+    assert not torch.equal(out[:, :, 300:], clean[:, :, 300:])
