@@ -38,7 +38,9 @@
 // causal over views, 404 causal; 43968 tokens causal over views and capped 7.1 ms (574
 // TFLOP/s of visible pairs).
 #include <algorithm>
+#include <cfloat>
 #include <climits>
+#include <cmath>
 
 #include "k_attn.cuh"
 #include "k_masked.cuh"
@@ -1150,13 +1152,19 @@ cudaError_t launch_masked_attn(const Dims &d, const MaskedAttnLaunch &a, cudaStr
   p.cap_log2 = m.softcap * kLog2e;
   p.cap_in = m.softcap > 0.f ? a.scale / m.softcap : 0.f;
   p.cap_half = 0.5f / p.cap_in;
-  // The fused cap: its coefficients must keep their range, and the bound that it takes for
-  // the row's maximum may lie 2 |z| above it, which costs the exponents that range: 64 at most.
+  // The fused cap: its coefficients, scale (scale / c)^2i times the fit's, must be normal fp32
+  // numbers, and the bound that it takes for the row's maximum may lie 2 |z| above it, which
+  // costs the exponents that range: 64 at most.
   p.cap_a = -1.f;
   if (p.cap_in > 1e-5f && p.cap_in < 1e5f) {
-    p.cap_a = std::min(0.375f / p.cap_in, 32.f / p.scale_log2);
+    bool normal = true;
     double k = (double)p.cap_log2 * p.cap_in;
-    for (int i = 0; i < 4; ++i, k *= (double)p.cap_in * p.cap_in) p.cap_k[i] = (float)(kTanhFit3[i] * k);
+    for (int i = 0; i < 4; ++i, k *= (double)p.cap_in * p.cap_in) {
+      const double x = std::abs(kTanhFit3[i] * k);
+      normal = normal && x >= FLT_MIN && x <= FLT_MAX;
+      p.cap_k[i] = normal ? (float)(kTanhFit3[i] * k) : 0.f;
+    }
+    if (normal) p.cap_a = std::min(0.375f / p.cap_in, 32.f / p.scale_log2);
   }
   unsigned char *ws = static_cast<unsigned char *>(a.workspace);
   int4 *blocks = reinterpret_cast<int4 *>(ws);

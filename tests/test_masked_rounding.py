@@ -167,3 +167,17 @@ def test_capped_rows_do_not_change_with_keys_that_they_do_not_see(hidden, bias, 
     out, lse2 = _run(q, k2, v2, kb, **mods)
     assert torch.equal(out[:, :, :300], clean[:, :, :300]) and torch.equal(lse2[:, :, :300], lse[:, :, :300])
     assert not torch.equal(out[:, :, 300:], clean[:, :, 300:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale,cap", [(1e10, 1.01e5), (1e30, 1.01e25), (3e-36, 4e-36), (1e-38, 1e-34), (0.125, 50.0)])
+def test_scales_and_caps_at_the_ends_of_their_ranges(scale, cap):
+    """Zero queries see every key alike, whatever the scale: the mean of the values."""
+    H, N = 4, 700
+    q, k, v = _inputs(H, N, N, seed=23)
+    out, lse = _run(q * 0, k, v, scale=scale, softcap=cap)
+    mean = v.double().mean(2, keepdim=True)
+    size = v.double().abs().mean(2, keepdim=True)
+    # the weights are exactly 1; sums of N values, the sum's reciprocal and the output's rounding
+    assert bool(((out.double() - mean).abs() <= 2.0 ** -8 * mean.abs() + (N + 64) * 2.0 ** -23 * size).all())
+    assert float((lse.double() - math.log(N)).abs().max()) <= 2.0 ** -20 + 2.0 ** -22 * math.log(N)
