@@ -1099,6 +1099,7 @@ KernelFn pick(bool cap, bool bias) {
 }  // namespace
 
 size_t masked_attn_workspace_bytes(const Dims &d, int q_len) {
+  if (masked_step_fits(d, q_len)) return 0;
   const int nq = (q_len + 127) / 128;
   const int splits = splits_of(d, nq);
   size_t n = plans_order(d, nq) ? 2 * round256(sizeof(int32_t) * (size_t)d.BH() * nq) : 0;

@@ -613,9 +613,10 @@ ress_status ress_masked_attn(const ress_shape *shape, const ress_attn_mods *mods
   if (d.B == 0 || m.q_len == 0) return RESS_OK;
   if (!ptr_ok(out)) return RESS_ERR_INVALID_ARG;
   if (d.N > 0) {
-    if (!ptr_ok(q) || !ptr_ok(k) || !ptr_ok(v) || !ptr_ok(workspace)) return RESS_ERR_INVALID_ARG;
+    const size_t need = ress::masked_attn_workspace_bytes(d, m.q_len);
+    if (!ptr_ok(q) || !ptr_ok(k) || !ptr_ok(v) || !aligned16(workspace)) return RESS_ERR_INVALID_ARG;
+    if (workspace_bytes < need || (need > 0 && workspace == nullptr)) return RESS_ERR_INVALID_ARG;
     if (!aligned16(kv_idx) || !aligned16(kv_cnt) || !aligned16(work_order)) return RESS_ERR_INVALID_ARG;
-    if (workspace_bytes < ress::masked_attn_workspace_bytes(d, m.q_len)) return RESS_ERR_INVALID_ARG;
   }
   ress::MaskedAttnLaunch a;
   a.mods = m;

@@ -169,8 +169,9 @@ class SparseGlobalAttention:
         block, for any q_len (new tokens over a cache).  Without `out`, the result goes to
         the layer's out and lse if q_len = N, else to a new tensor (made on `stream`; the
         current stream has to wait for the call before it reads it).  The layer keeps one
-        workspace per number of query blocks, for eager calls and captured graphs alike:
-        such calls of one layer must not overlap in time."""
+        workspace per number of query blocks (up to 40 MB, for as long as it lives; none for
+        few rows), for eager calls and captured graphs alike: such calls of one layer must
+        not overlap in time."""
         n = q.shape[2]
         if kept and n != self.N:
             raise ValueError("the kept blocks are those of the sequence's own tokens")
@@ -179,14 +180,18 @@ class SparseGlobalAttention:
                 out, lse = self.out, self.lse if lse is None else lse
             else:
                 out = self._empty((self.B, self.H, n, 64), torch.bfloat16, stream)
-        ws = self._masked_ws.get((n + 127) // 128)
-        if ws is None:
-            need = R.ress_masked_attn_workspace_bytes(self.shape, (n + 127) // 128 * 128)
-            ws = self._empty((max(need, 16),), torch.uint8, stream)
+        # (calls of few rows take none; the others' size goes by the query blocks)
+        need = R.ress_masked_attn_workspace_bytes(self.shape, n)
+        ws = None
+        if need:
+            ws = self._masked_ws.get((n + 127) // 128)
+            if ws is None:
+                ws = self._empty((need,), torch.uint8, stream)
         R.ress_masked_attn(self.shape, q, k, v, self.kv_idx if kept else None,
                            self.kv_cnt if kept else None, None, self.scale, out, lse, workspace=ws,
                            dev_err=self.dev_err[:1], stream=stream, **mods)
-        self._masked_ws[(n + 127) // 128] = ws  # kept for good: a captured graph holds its address
+        if need:
+            self._masked_ws[(n + 127) // 128] = ws  # kept for good: a captured graph holds its address
         return out
 
     def forward(self, q, k, v, method: int, budgets: Sequence[int], keep_k=None, dense_q=None,

@@ -472,7 +472,8 @@ def ress_masked_attn(shape, q, k, v, kv_idx, kv_cnt, work_order, scale: float, o
                      stream=None):
     """Attention over kept blocks with capped scores, a distance bias and document and order
     masks, for all tokens or for others: q [B,H,q_len,64] over k, v [B,H,N,64].  kv_idx and
-    kv_cnt None: every key block.  `workspace`: uint8, ress_masked_attn_workspace_bytes."""
+    kv_cnt None: every key block.  `workspace`: uint8, ress_masked_attn_workspace_bytes (None
+    where that is 0)."""
     s = _shape(shape)
     dev = q.device
     if q.dim() != 4:

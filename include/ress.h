@@ -541,7 +541,8 @@ typedef struct {
                                      max(0, index - prefix + 1) for a prefix seen by all     */
 } ress_attn_mods;
 
-/* Bytes of device workspace that ress_masked_attn needs for `shape` with q_len query tokens. */
+/* Bytes of device workspace that ress_masked_attn needs for `shape` with exactly q_len query
+ * tokens; 0 where it needs none (few query rows). */
 size_t ress_masked_attn_workspace_bytes(const ress_shape *shape, int32_t q_len);
 
 /*
@@ -568,7 +569,7 @@ size_t ress_masked_attn_workspace_bytes(const ress_shape *shape, int32_t q_len);
  *   mods     HOST; NULL: q_len = N and scores as they are.
  *   workspace  DEVICE scratch of at least ress_masked_attn_workspace_bytes(shape, q_len)
  *            bytes, 16-byte aligned, overwritten; calls that may overlap in time need one
- *            each.
+ *            each.  NULL where that is 0.
  *   dev_err  as for ress_block_sparse_attn (a row with a bad list is left unwritten).
  * N = 0 with q_len > 0 writes zero rows and lse = -inf (no workspace needed).
  */
