@@ -33,10 +33,10 @@
 //
 // What bounds it: as in k_attn.cu the softmax warps, two a scheduler, whose dependent chains do
 // not hide one another; the exponentials alone take 1024 of about 1870 clocks per tile and SM.
-// Measured on one B200, 16 heads x 10992 tokens, every block: 754 us plain (653 TFLOP/s), 902
-// with a bias by view, 908 capped at 50, 1780 capped at 10 (scores beyond the polynomials), 464
-// causal over views, 404 causal; 43968 tokens causal over views and capped 7.1 ms (574
-// TFLOP/s of visible pairs).
+// Measured on one B200, 16 heads x 10992 tokens, every block: 755 us plain (653 TFLOP/s), 908
+// with a bias by view, 960 by token, 922 capped at 50, 2100 capped at 10 (scores beyond the
+// polynomials), 1470 capped at 50 with a bias by view, 458 causal over views, 398 causal; 43968
+// tokens causal over views and capped 7.1-7.2 ms (570 TFLOP/s of visible pairs).
 #include <algorithm>
 #include <cfloat>
 #include <climits>

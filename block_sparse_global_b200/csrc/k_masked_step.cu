@@ -9,9 +9,8 @@
 // computed), keep an online softmax per lane group in fp32, and join over lanes, warps and,
 // through distributed shared memory, the cluster.  One launch, no workspace.
 //
-// Measured, one token over 16 heads, in a CUDA graph: 10992 tokens (45 MB) 14.4 us, 43968
-// tokens (180 MB) 47 us; 128 heads over 10992 tokens (360 MB) 62 us = 5.8 TB/s.  About 6 us
-// of each are launch and joins.  Two CTAs of 384 threads an SM: a cluster of eight CTAs that
+// Measured, one token over 10992, in a CUDA graph: 16 heads (45 MB) 14.4 us, 128 heads (360 MB)
+// 59 us = 6.1 TB/s.  About 6 us of each are launch and joins.  Two CTAs of 384 threads an SM: a cluster of eight CTAs that
 // fill an SM each does not fit every GPC beside the others (512 threads, one an SM: 18 us);
 // a ring of asynchronous copies in shared memory was slower (19 us).
 #include <cooperative_groups.h>
@@ -232,9 +231,10 @@ int step_parts(long long rows, int N) {
 
 // Which form takes a call.  Measured: this one takes 6 us and about 8.1 ns for every key that
 // a resident CTA walks; the tensor-core form 16 us and what the keys and values of all heads
-// take at 6 TB/s, whatever the queries of a block.  (16 heads: one token over 10992 keys 15
-// against 23 us, over 43968 51 against 46; 2 tokens over 10992 16 against 22, 3 tokens 28
-// against 22; 16 tokens over 1000 keys 13 against 18.)
+// take at 6 TB/s, whatever the queries of a block.  (16 heads, in a CUDA graph, this form
+// against the other: one token over 10992 keys 14 against 19 us, over 43968 46 against 41; 2
+// tokens over 10992 15 against 19, 3 tokens 25 against 18; 16 tokens over 1000 keys 12 and 12,
+// back to back from the host 13 against 18; 128 heads, one token over 10992 59 against 76.)
 bool masked_step_fits(const Dims &d, int q_len) {
   const long long rows = d.BH() * q_len;
   const int parts = step_parts(rows, d.N);

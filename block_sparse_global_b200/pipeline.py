@@ -202,7 +202,10 @@ class SparseGlobalAttention:
         otherwise; with fused=False, DRIFT runs the separate block-map, drift and selection
         calls) -> schedule -> attention.  write_scores: the fused kernels also write P,
         v_bar (and s for DRIFT).  mods: the attention is attend_masked() with these changes of
-        the scores (the selection does not see them)."""
+        the scores.  The selection does not see them: under document or order masks part of a
+        row's budget may go to blocks that its queries do not see, and a query whose kept
+        blocks are all hidden from it gets a zero row and lse = -inf although it sees keys
+        elsewhere.  keep_k, dense_q and the budgets are the caller's means against that."""
         self.pool(q, k, v, stream)
         if method == R.SELECT_DRIFT and fused:
             self.drift_select(budgets, keep_k, dense_q, rounds, rho, eps, stream,

@@ -561,7 +561,9 @@ size_t ress_masked_attn_workspace_bytes(const ress_shape *shape, int32_t q_len);
  *            or NULL.
  *   kv_idx   int32 [B,H,nq,nk] and kv_cnt int32 [B,H,nq], as for ress_block_sparse_attn; or
  *            both NULL: every key block is kept.  Blocks that no query of a row sees are
- *            passed over unread.  A block listed twice counts twice.
+ *            passed over unread.  A block listed twice counts twice.  The selection calls
+ *            know of no masks: a query that sees none of its row's kept blocks has a zero row
+ *            whatever it would see in the others.
  *   work_order int32 [B*H*nq] permutation or NULL: an order of the library's own (rows that
  *            see most first, where that pays).  Outputs do not depend on it.  Calls of few
  *            rows do not look at it; otherwise an entry out of range is reported by dev_err.
