@@ -497,9 +497,10 @@ ress_status ress_rope(const ress_rope_plan *plan, int32_t batch, int32_t heads, 
   if (!plan_ok(plan) || batch < 0 || heads < 0 || tokens < 0) return RESS_ERR_INVALID_ARG;
   if (inverse != 0 && inverse != 1) return RESS_ERR_INVALID_ARG;
   const size_t size = dtype_bytes(dtype);
-  if (size == 0 || !positions_ok(plan, positions, pos_stride_b)) return RESS_ERR_INVALID_ARG;
+  if (size == 0) return RESS_ERR_INVALID_ARG;
   if (heads > kMaxTokenHeads) return RESS_ERR_UNSUPPORTED;
   if (batch == 0 || heads == 0 || tokens == 0) return RESS_OK;
+  if (!positions_ok(plan, positions, pos_stride_b)) return RESS_ERR_INVALID_ARG;
   if (!rows_ok(x, size) || !out_rows_ok(out, size, batch, heads, tokens, plan->head_dim))
     return RESS_ERR_INVALID_ARG;
   if (x->ptr == out->ptr && !same_rows(x, out, batch, heads, tokens)) return RESS_ERR_INVALID_ARG;
@@ -533,15 +534,13 @@ ress_status ress_qk_norm_rope(const ress_qk_params *params, const ress_rows *q,
   if (!(p.eps >= 0.f) || std::isinf(p.eps)) return RESS_ERR_INVALID_ARG;
   for (const float *w : {p.q_weight, p.q_bias, p.k_weight, p.k_bias})
     if (!aligned_to(w, 4)) return RESS_ERR_INVALID_ARG;
-  if (p.rope != nullptr) {
-    if (!plan_ok(p.rope) || p.rope->head_dim != p.head_dim) return RESS_ERR_INVALID_ARG;
-    if (!positions_ok(p.rope, p.positions, p.pos_stride_b)) return RESS_ERR_INVALID_ARG;
-  }
+  if (p.rope != nullptr && (!plan_ok(p.rope) || p.rope->head_dim != p.head_dim)) return RESS_ERR_INVALID_ARG;
   if (p.views < 1 || p.specials < 0 || p.tokens % p.views != 0 || p.specials > p.tokens / p.views)
     return RESS_ERR_INVALID_ARG;
   if ((v == nullptr) != (v_out == nullptr)) return RESS_ERR_INVALID_ARG;
   if (p.q_heads > kMaxTokenHeads || p.kv_heads > kMaxTokenHeads) return RESS_ERR_UNSUPPORTED;
   if (p.batch == 0 || p.tokens == 0) return RESS_OK;
+  if (p.rope != nullptr && !positions_ok(p.rope, p.positions, p.pos_stride_b)) return RESS_ERR_INVALID_ARG;
   const bool moves = p.specials > 0 && p.specials < p.tokens / p.views;  // some token's place changes
   const ress_rows *in[3] = {q, k, v}, *out[3] = {q_out, k_out, v_out};
   const int heads[3] = {p.q_heads, p.kv_heads, p.kv_heads};
@@ -600,15 +599,16 @@ ress_status ress_masked_attn(const ress_shape *shape, const ress_attn_mods *mods
   if (m.q_len < 0 || !(m.softcap >= 0.f)) return RESS_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !(scale <= 1e30f) || !(m.softcap <= 1e30f)) return RESS_ERR_INVALID_ARG;
   if (m.softcap > 0.f && !(scale / m.softcap >= 1e-20f && scale / m.softcap <= 1e20f)) return RESS_ERR_INVALID_ARG;
-  if ((m.q_pos == nullptr) != (m.k_pos == nullptr) || (m.q_doc == nullptr) != (m.k_doc == nullptr) ||
-      (m.q_order == nullptr) != (m.k_order == nullptr))
-    return RESS_ERR_INVALID_ARG;
-  if (m.slopes != nullptr && m.q_pos == nullptr) return RESS_ERR_INVALID_ARG;
+  if (d.N > 0 && m.q_len > 0 && d.B > 0) {  // (an array without elements may be NULL)
+    if ((m.q_pos == nullptr) != (m.k_pos == nullptr) || (m.q_doc == nullptr) != (m.k_doc == nullptr) ||
+        (m.q_order == nullptr) != (m.k_order == nullptr) || (kv_idx == nullptr) != (kv_cnt == nullptr))
+      return RESS_ERR_INVALID_ARG;
+    if (m.slopes != nullptr && m.q_pos == nullptr) return RESS_ERR_INVALID_ARG;
+  }
   for (const void *x : {(const void *)m.slopes, (const void *)m.q_pos, (const void *)m.k_pos, (const void *)m.q_doc,
                         (const void *)m.k_doc, (const void *)m.q_order, (const void *)m.k_order, (const void *)lse,
                         (const void *)dev_err})
     if (!aligned_to(x, 4)) return RESS_ERR_INVALID_ARG;
-  if ((kv_idx == nullptr) != (kv_cnt == nullptr)) return RESS_ERR_INVALID_ARG;
   if (!queries_ok(d, m.q_len)) return RESS_ERR_UNSUPPORTED;
   if (d.B == 0 || m.q_len == 0) return RESS_OK;
   if (!ptr_ok(out)) return RESS_ERR_INVALID_ARG;
