@@ -505,8 +505,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           // queries: shift[i] + step[i] (c mod 64 - end) if positions run evenly in each half
           // (the usual case: tokens, or all of one view), else shift[i] + m_pos[c].  end is
           // the column of a half's key nearest to the queries, 0 or 63; m_pos is measured from
-          // the warp's query nearest to the keys: both terms have the distance's sign,
-          // and neither is larger, so that nothing cancels however far the tile reaches and
+          // the warp's query nearest to the keys: both terms have the distance's sign, and
+          // neither is larger, so that nothing cancels however far the tile reaches and
           // wherever the block's other queries are.  On both sides, from the middle of all
           // of the positions: differences from it are exact up to the documented 2^24.
           float shift[2] = {0.f, 0.f}, step[2] = {0.f, 0.f};

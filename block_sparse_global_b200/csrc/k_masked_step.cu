@@ -10,9 +10,9 @@
 // through distributed shared memory, the cluster.  One launch, no workspace.
 //
 // Measured, one token over 10992, in a CUDA graph: 16 heads (45 MB) 14.4 us, 128 heads (360 MB)
-// 59 us = 6.1 TB/s.  About 6 us of each are launch and joins.  Two CTAs of 384 threads an SM: a cluster of eight CTAs that
-// fill an SM each does not fit every GPC beside the others (512 threads, one an SM: 18 us);
-// a ring of asynchronous copies in shared memory was slower (19 us).
+// 59 us = 6.1 TB/s.  About 6 us of each are launch and joins.  Two CTAs of 384 threads an SM: a
+// cluster of eight CTAs that fill an SM each does not fit every GPC beside the others (512
+// threads, one an SM: 18 us); a ring of asynchronous copies in shared memory was slower (19 us).
 #include <cooperative_groups.h>
 
 #include <algorithm>
